@@ -8,6 +8,7 @@
 #include "common.cuh"
 #include "gemm.cuh"
 #include "mosaic_test.h"
+#include "ops.cuh"
 
 namespace mq {
 
@@ -135,6 +136,14 @@ static mq_status launched(cudaError_t e, int kernels) {
     g_launches.fetch_add((uint64_t)kernels, std::memory_order_relaxed);
     return MQ_OK;
 }
+
+namespace mq {
+
+// For the operators of ops.cu.
+mq_status count_launches(cudaError_t e, int kernels) { return launched(e, kernels); }
+int* device_error_word() { return err_word(); }
+
+}  // namespace mq
 
 static bool nvfp4_shape_ok(int rows, int cols) { return rows > 0 && cols > 0 && cols % 64 == 0; }
 

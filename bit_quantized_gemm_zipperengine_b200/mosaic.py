@@ -31,7 +31,13 @@ EXPORTED = (
     "mq_gemm_noalloc", "mq_gemm_noalloc_scratch_limit", "mq_quantize_weight_delta", "mq_topk_blocks",
     "mq_pack_residual_weight", "mq_gemm_act", "mq_weight_bytes", "mq_fp4_mma_loop", "mq_fp4_mma_loop_flops",
     "mq_test_arm_wait_fault", "mq_smooth_scales", "mq_smooth_apply", "mq_timeline_read",
+    "mq_kv_cache_bytes", "mq_gemv", "mq_qk_norm_rope", "mq_kv_append", "mq_qkv_append", "mq_kv_read",
+    "mq_kv_attention_workspace_bytes", "mq_kv_attention",
 )
+
+MQ_BF16 = 0
+MQ_F16 = 1
+GEMV_MAX_TOKENS = 16
 
 
 class MosaicError(RuntimeError):
@@ -55,6 +61,12 @@ class LayerBuffers(ctypes.Structure):
                 ("packed", ResidualPacked), ("ws_quant", ctypes.c_void_p), ("ws_quant_bytes", ctypes.c_size_t),
                 ("ws_gemm", ctypes.c_void_p), ("ws_gemm_bytes", ctypes.c_size_t), ("W_dev", ctypes.c_void_p),
                 ("X_dev", ctypes.c_void_p), ("Xcal_dev", ctypes.c_void_p), ("Y_dev", ctypes.c_void_p)]
+
+
+class KVCacheStruct(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("heads", ctypes.c_int), ("D", ctypes.c_int), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
 
 
 def lib():
@@ -119,6 +131,19 @@ def lib():
     L.mq_status_string.restype = ctypes.c_char_p
     L.mq_launch_count.argtypes = []
     L.mq_launch_count.restype = ctypes.c_uint64
+    i64, u32, f32 = ctypes.c_int64, ctypes.c_uint, ctypes.c_float
+    L.mq_kv_cache_bytes.argtypes = [i32] * 4
+    L.mq_kv_cache_bytes.restype = sz
+    L.mq_kv_attention_workspace_bytes.argtypes = [i32] * 4
+    L.mq_kv_attention_workspace_bytes.restype = sz
+    L.mq_gemv.argtypes = [vp, i32, i64, vp, vp, vp, i64, i32, i32, i32, u32, vp]
+    L.mq_qk_norm_rope.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp, f32, vp, vp, i32, i32, vp]
+    L.mq_kv_append.argtypes = [vp, vp, i32, i32, vp, vp, vp]
+    L.mq_qkv_append.argtypes = [vp, vp, vp, vp, vp, i32, i32, vp, vp, f32, vp, vp, i32, i32, vp, vp, vp]
+    L.mq_kv_read.argtypes = [vp, vp, i32, vp, vp, i32, vp]
+    L.mq_kv_attention.argtypes = [vp, vp, vp, i32, i32, vp, vp, i64, i32, i32, vp, i32, vp, f32, i32, vp, sz, vp]
+    for f in ("mq_gemv", "mq_qk_norm_rope", "mq_kv_append", "mq_qkv_append", "mq_kv_read", "mq_kv_attention"):
+        getattr(L, f).restype = i32
     _lib = L
     return L
 
@@ -320,6 +345,224 @@ def gemm_workspace(M: int, N: int, K: int, flags: int, device) -> torch.Tensor |
     return torch.zeros(max(n, 16), dtype=torch.uint8, device=device) if n else None
 
 
+# ------------------------------------------------------------------ mosaic_ops.h
+_TYPES = {torch.bfloat16: MQ_BF16, torch.float16: MQ_F16}
+
+
+class _on:
+    """The call's stream as an integer, with the tensors' device current inside the block
+    (a launch on another device's stream would fail). Without a stream argument: that
+    device's current stream."""
+
+    __slots__ = ("dev", "back", "stream")
+
+    def __init__(self, t: torch.Tensor, stream=None):
+        if not t.is_cuda:
+            raise MosaicError("libmosaic takes CUDA tensors only")
+        self.dev = t.get_device()
+        self.stream = (torch._C._cuda_getCurrentRawStream(self.dev) if stream is None else stream.cuda_stream)
+
+    def __enter__(self):
+        here = torch.cuda.current_device()
+        self.back = None
+        if here != self.dev:
+            self.back = here
+            torch.cuda.set_device(self.dev)
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+        return False
+
+
+def _type(t: torch.Tensor, *others) -> int:
+    """The mq_dtype of 16-bit tensors, all of one type and device."""
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise MosaicError(f"bf16 or fp16 tensors are taken, not {t.dtype}")
+    for o in others:
+        if o is not None and (o.dtype != t.dtype or o.device != t.device):
+            raise MosaicError(f"one type and device per call: {t.dtype} on {t.device} and {o.dtype} on {o.device}")
+    return code
+
+
+def _index(t: torch.Tensor, dtype, numel: int, like: torch.Tensor, what: str) -> int:
+    """Pointer of a contiguous index array of at least numel elements."""
+    if t.dtype != dtype or t.device != like.device or t.numel() < numel or not t.is_contiguous():
+        raise MosaicError(f"{what}: {numel} contiguous {dtype} values on {like.device} are wanted, got {t.dtype} "
+                          f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+class _heads:
+    """The mq_heads of several [T][heads][D] tensors in one block of memory; at(i) is the
+    address of the i-th (None for an absent one)."""
+
+    __slots__ = ("buf", "base", "have")
+
+    def __init__(self, T: int, D: int, *ts):
+        v = []
+        for t in ts:
+            if t is None:
+                v += (0, 0, 0, 0)
+                continue
+            n, h, d = t.shape
+            st, sh, sd = t.stride()
+            if n != T or d != D or sd != 1:
+                raise MosaicError(f"[{T}][heads][{D}] with adjacent elements is wanted, got shape {tuple(t.shape)}, "
+                                  f"strides {t.stride()}")
+            v += (t.data_ptr(), h, st, sh)
+        self.buf = (ctypes.c_int64 * len(v))(*v)
+        self.base = ctypes.addressof(self.buf)
+        self.have = [t is not None for t in ts]
+
+    def at(self, i: int):
+        return self.base + 32 * i if self.have[i] else None
+
+
+class Weight:
+    """A packed weight (base, and optionally its residual blocks) with the C structs that
+    the calls take, built once. Keeps the tensors alive."""
+
+    def __init__(self, base: dict, packed: dict | None = None):
+        self.N, self.K = base["rows"], base["cols"]
+        self.base, self.packed = base, packed
+        self._mat, self._res = mat(base), packed_struct(packed)
+        self.base_ptr = ctypes.addressof(self._mat)
+        self.packed_ptr = None if self._res is None else ctypes.addressof(self._res)
+
+
+class KVCache:
+    """A paged NVFP4 key/value cache (include/mosaic_ops.h, mq_kv_cache) over a byte tensor
+    [pages][heads][page_size / 16][18 D]; k_scale, v_scale: fp32 [heads] or None (1.0)."""
+
+    def __init__(self, pages: torch.Tensor, k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None):
+        if pages.dtype != torch.uint8 or pages.dim() != 4 or not pages.is_contiguous() or pages.shape[3] not in (1152, 2304):
+            raise MosaicError("pages: a contiguous uint8 tensor [pages][heads][page_size / 16][18 D], D = 64 or 128")
+        self.pages, self.k_scale, self.v_scale = pages, k_scale, v_scale
+        self.num_pages, self.heads, self.D = pages.shape[0], pages.shape[1], pages.shape[3] // 18
+        self.page_size = 16 * pages.shape[2]
+        for s in (k_scale, v_scale):
+            if s is not None:
+                _index(s, torch.float32, self.heads, pages, "tensor scales")
+        self._struct = KVCacheStruct(_ptr(pages), self.num_pages, self.page_size, self.heads, self.D, _ptr(k_scale),
+                                     _ptr(v_scale))
+        self.ptr = ctypes.addressof(self._struct)
+
+    @classmethod
+    def alloc(cls, num_pages: int, page_size: int, heads: int, D: int, device="cuda", k_scale=None, v_scale=None):
+        if lib().mq_kv_cache_bytes(num_pages, page_size, heads, D) == 0:
+            raise MosaicError(f"bad cache shape: {num_pages} pages of {page_size}, {heads} heads, D = {D}")
+        return cls(torch.zeros((num_pages, heads, page_size // 16, 18 * D), dtype=torch.uint8, device=device), k_scale,
+                   v_scale)
+
+
+def mq_gemv(X: torch.Tensor, w: Weight, Y: torch.Tensor, flags: int = 0, stream=None):
+    """Y [M][N] = X [M][K] times the packed weight, X in 16 bits (not quantized), M <= 16."""
+    ty = _type(X, Y)
+    (M, K), (My, N) = X.shape, Y.shape
+    if K != w.K or N != w.N or My != M or X.stride(1) != 1 or Y.stride(1) != 1:
+        raise MosaicError(f"mq_gemv: X [M][{w.K}] and Y [M][{w.N}] are wanted, got {tuple(X.shape)} and {tuple(Y.shape)}")
+    with _on(X, stream) as s:
+        st = lib().mq_gemv(X.data_ptr(), ty, X.stride(0), w.base_ptr, w.packed_ptr, Y.data_ptr(), Y.stride(0), M, N, K,
+                           flags, s)
+    _check(st, "mq_gemv")
+
+
+def _turn(T, pos, freq, like):
+    """(pos pointer, freq pointer, rot) of a rotation; freq None: no rotation."""
+    if freq is None:
+        return None, None, 0
+    return _index(pos, torch.int64, T, like, "pos"), _index(freq, torch.float64, 1, like, "freq"), 2 * freq.numel()
+
+
+def _norm_weight(w, D, like):
+    if w is None:
+        return None
+    return _index(w, like.dtype, D, like, "norm weight")
+
+
+def mq_qk_norm_rope(q, k, q_out, k_out, pos=None, freq=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                    interleaved: bool = False, stream=None):
+    """Head norms and the rotation of q [T][heads][D] and k (either may be None); the
+    outputs may be the inputs. freq: fp64 [rot / 2] radians a position."""
+    x = q if q is not None else k
+    ty = _type(x, q, k, q_out, k_out)
+    T, _, D = x.shape
+    h = _heads(T, D, q, k, q_out, k_out)
+    pp, fp, rot = _turn(T, pos, freq, x)
+    with _on(x, stream) as s:
+        st = lib().mq_qk_norm_rope(h.at(0), h.at(1), h.at(2), h.at(3), T, D, ty, _norm_weight(q_weight, D, x),
+                                   _norm_weight(k_weight, D, x), eps, pp, fp, rot, interleaved, s)
+    _check(st, "mq_qk_norm_rope")
+
+
+def mq_kv_append(k, v, slots, cache: KVCache, stream=None):
+    """Rows k, v [T][heads][D] into the cache at slots (int64 [T], negative: skipped)."""
+    ty = _type(k, v)
+    T = k.shape[0]
+    h = _heads(T, cache.D, k, v)
+    with _on(cache.pages, stream) as s:
+        st = lib().mq_kv_append(h.at(0), h.at(1), T, ty, _index(slots, torch.int64, T, k, "slots"), cache.ptr, s)
+    _check(st, "mq_kv_append")
+
+
+def mq_qkv_append(q, k, v, q_out, slots, cache: KVCache, pos=None, freq=None, q_weight=None, k_weight=None,
+                  eps: float = 1e-6, interleaved: bool = False, k_out=None, stream=None):
+    """mq_qk_norm_rope and mq_kv_append in one launch (the turned keys go to the cache, and
+    to k_out if given)."""
+    ty = _type(q, k, v, q_out, k_out)
+    T = q.shape[0]
+    h = _heads(T, cache.D, q, k, v, q_out, k_out)
+    pp, fp, rot = _turn(T, pos, freq, q)
+    with _on(cache.pages, stream) as s:
+        st = lib().mq_qkv_append(h.at(0), h.at(1), h.at(2), h.at(3), h.at(4), T, ty, _norm_weight(q_weight, cache.D, q),
+                                 _norm_weight(k_weight, cache.D, q), eps, pp, fp, rot, interleaved,
+                                 _index(slots, torch.int64, T, q, "slots"), cache.ptr, s)
+    _check(st, "mq_qkv_append")
+
+
+def mq_kv_read(cache: KVCache, slots, k, v, stream=None):
+    """The cached rows of slots (int64 [T]) as 16-bit k, v [T][heads][D]."""
+    ty = _type(k, v)
+    T = k.shape[0]
+    h = _heads(T, cache.D, k, v)
+    with _on(cache.pages, stream) as s:
+        st = lib().mq_kv_read(cache.ptr, _index(slots, torch.int64, T, k, "slots"), T, h.at(0), h.at(1), ty, s)
+    _check(st, "mq_kv_read")
+
+
+def kv_attention_workspace(q: torch.Tensor, cache: KVCache, max_q: int = 1) -> torch.Tensor | None:
+    """Zeroed workspace for mq_kv_attention with q's heads (see include/mosaic_ops.h)."""
+    with _on(q):
+        n = lib().mq_kv_attention_workspace_bytes(q.shape[1], cache.heads, cache.D, max_q)
+    return torch.zeros(n, dtype=torch.uint8, device=q.device) if n else None
+
+
+def mq_kv_attention(q, cache: KVCache, block_table, kv_len, out, scale: float, cu_q=None, max_q: int = 1,
+                    window: int = 0, lse=None, ws=None, stream=None):
+    """out [T][heads][D] = attention of q over the cached tokens. block_table: int32 [B][pages],
+    kv_len: int32 [B], cu_q: int32 [B + 1] or None (one query token a sequence), lse: fp32
+    [T][heads] or None, ws: kv_attention_workspace(q, cache, max_q)."""
+    ty = _type(q, out)
+    T, B = q.shape[0], kv_len.shape[0]
+    h = _heads(T, cache.D, q, out)
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.device != q.device or \
+            block_table.shape[0] < B or block_table.stride(1) != 1:
+        raise MosaicError("block_table: int32 [B][pages] on q's device")
+    if lse is not None:
+        _index(lse, torch.float32, T * q.shape[1], q, "lse")
+    with _on(cache.pages, stream) as s:
+        st = lib().mq_kv_attention(
+            h.at(0), h.at(1), None if lse is None else lse.data_ptr(), T, ty, cache.ptr, block_table.data_ptr(),
+            block_table.stride(0), block_table.shape[1], B,
+            None if cu_q is None else _index(cu_q, torch.int32, B + 1, q, "cu_q"), max_q,
+            _index(kv_len, torch.int32, B, q, "kv_len"), scale, window, None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel(), s)
+    _check(st, "mq_kv_attention")
+
+
 # ------------------------------------------------------------------ convenience
 class Layer:
     """One linear layer through the whole path: quantize W, H from calibration tokens,
@@ -399,3 +642,66 @@ class Layer:
         mq_quantize_act(X, xq, stream)
         mq_gemm(xq, self.base, self.packed, Y, M, self.N, self.K, flags, ws, stream)
         return Y
+
+    @property
+    def weight(self) -> Weight:
+        """The packed weight as mq_gemv takes it (built once; it reads the same buffers)."""
+        if not hasattr(self, "_weight"):
+            self._weight = Weight(self.base, self.packed)
+        return self._weight
+
+    def forward_16bit(self, X: torch.Tensor, out: torch.Tensor | None = None, flags: int = 0, stream=None):
+        """X [M][K] in bf16 or fp16, M <= 16, times the packed weight without quantizing X
+        (mq_gemv): a new tensor, or out."""
+        Y = torch.empty((X.shape[0], self.N), dtype=X.dtype, device=X.device) if out is None else out
+        mq_gemv(X, self.weight, Y, flags, stream)
+        return Y
+
+
+class AttentionLayer:
+    """The attention half of a decoder layer on quantized weights and a 4-bit cache:
+    qkv projection, head norms + rotation + cache append, attention, out projection.
+
+    qkv: a Layer of (q_heads + 2 kv_heads) * D rows (queries, keys, values); out: a Layer of
+    q_heads * D columns; freq: fp64 [rot / 2]; q_norm, k_norm: [D] weights or None."""
+
+    def __init__(self, qkv: Layer, out: Layer, q_heads: int, cache: KVCache, freq, q_norm=None, k_norm=None,
+                 eps: float = 1e-6, interleaved: bool = False, scale: float | None = None, window: int = 0):
+        D, H = cache.D, cache.heads
+        if qkv.N != (q_heads + 2 * H) * D or out.K != q_heads * D:
+            raise MosaicError(f"qkv must have {(q_heads + 2 * H) * D} rows and out {q_heads * D} columns")
+        self.qkv, self.out, self.q_heads, self.cache = qkv, out, q_heads, cache
+        self.freq, self.q_norm, self.k_norm, self.eps, self.interleaved = freq, q_norm, k_norm, eps, interleaved
+        self.scale = D ** -0.5 if scale is None else scale
+        self.window = window
+        self._ws = {}
+
+    def _project(self, layer: Layer, X):
+        # up to 16 tokens the weight's bytes bound the product: X stays in 16 bits
+        if X.shape[0] <= GEMV_MAX_TOKENS:
+            return layer.forward_16bit(X)
+        if X.dtype != torch.bfloat16:
+            raise MosaicError("more than 16 tokens are taken in bf16")
+        return layer.forward(X)
+
+    def step(self, X, pos, slots, block_table, kv_len, cu_q=None, max_q: int = 1, stream=None):
+        """One pass of the T new tokens X [T][hidden] (bf16; fp16 up to 16 tokens): their keys
+        and values are appended at slots, then they attend to their sequences. kv_len counts
+        them. Tokens of one sequence are adjacent (cu_q). Every stream has its own workspace,
+        so calls of up to 16 tokens may overlap on different streams; calls of more tokens use
+        the layers' own buffers (see Layer.forward) and must not."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.step(X, pos, slots, block_table, kv_len, cu_q, max_q)
+        T, D, H, Hq = X.shape[0], self.cache.D, self.cache.heads, self.q_heads
+        y = self._project(self.qkv, X).view(T, Hq + 2 * H, D)
+        q, k, v = y[:, :Hq], y[:, Hq:Hq + H], y[:, Hq + H:]
+        mq_qkv_append(q, k, v, q, slots, self.cache, pos, self.freq, self.q_norm, self.k_norm, self.eps,
+                      self.interleaved)
+        o = torch.empty((T, Hq, D), dtype=X.dtype, device=X.device)
+        key = (max_q, torch.cuda.current_stream(X.device))
+        if key not in self._ws:
+            self._ws[key] = kv_attention_workspace(q, self.cache, max_q)
+        mq_kv_attention(q, self.cache, block_table, kv_len, o, self.scale, cu_q, max_q, self.window, None,
+                        self._ws[key])
+        return self._project(self.out, o.view(T, Hq * D))

@@ -1,0 +1,490 @@
+"""The operators of include/mosaic_ops.h on the GPU against plain 64-bit references: odd
+sizes, strides, pages, ragged lengths, empty rows, NaN in places that no row sees, both
+types, captured graphs, other streams, and a decoder layer's attention half run through
+all of them. Quantized results are compared bit for bit with the CPU oracle."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import ops_ref as ref
+import synth
+from gpu_path import to_dev
+
+pytestmark = pytest.mark.gpu
+BF, HF = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return torch.device("cuda:0")
+
+
+@pytest.fixture(scope="module")
+def mosaic():
+    from bit_quantized_gemm_zipperengine_b200 import mosaic as m
+    return m
+
+
+@pytest.fixture(autouse=True)
+def no_device_error(request):
+    yield
+    from bit_quantized_gemm_zipperengine_b200 import mosaic
+    assert mosaic.mq_get_error() == 0
+
+
+def within(got, want, bound, what=""):
+    err = (got.double() - want).abs()
+    bad = ~(err <= bound)
+    assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.numel()} off, worst {float((err / bound)[bad].max()):.2f} x "
+                           f"the bound, first at {torch.nonzero(bad)[0].tolist()}")
+
+
+# ------------------------------------------------------------------------------ mq_gemv
+def gemv_bound(x, W, y, g, dtype, K):
+    """One rounding of the result, and the fp32 sum: K/16 accumulations of 16-element products
+    (a tensor-core accumulation may truncate: 2^-23 of the running magnitude each), with 64
+    more steps of 2^-24 for the sums between warps and the scale."""
+    mag = (x.double().abs() @ W.abs().t()) * abs(g)
+    e = (K / 8 + 64) * 2.0 ** -24 * mag
+    return ref.rounding(y.abs() + e, dtype) + e
+
+
+@pytest.mark.parametrize("M", [1, 2, 7, 8, 9, 16])
+@pytest.mark.parametrize("N,K,budget", [(64, 64, 0), (64, 64, 1), (192, 320, 7), (128, 4096, 40), (576, 192, 27),
+                                        (1024, 1088, 100), (256, 14336, 300)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_gemv(M, N, K, budget, dtype, dev, mosaic):
+    base, packed = ref.random_weight(N, K, budget, 11 * N + K, dev)
+    gen = torch.Generator().manual_seed(M)
+    hot = 1 + 29 * (torch.rand(K, generator=gen) < 0.02)
+    x = (torch.randn(M, K, generator=gen) * hot * 0.1).to(dtype).to(dev)
+    y = torch.full((M, N), math.nan, dtype=dtype, device=dev)
+    mosaic.mq_gemv(x, mosaic.Weight(base, packed), y)
+    W, g = ref.dense_weight(base, packed), float(base["gscale"])
+    want = x.double() @ W.t() * g
+    within(y, want, gemv_bound(x, W, want, g, dtype, K), f"M={M} {N}x{K}")
+
+
+@pytest.mark.parametrize("mode", ["base", "residual"])
+def test_gemv_parts_strides_flags(mode, dev, mosaic):
+    N, K, M = 320, 704, 5
+    base, packed = ref.random_weight(N, K, 20, 5, dev)
+    big = torch.randn(M, K + 264, generator=torch.Generator().manual_seed(1)).to(BF).to(dev)
+    x = big[:, 8:8 + K]
+    out = torch.full((M, N + 7), 9.0, dtype=BF, device=dev)
+    y = out[:, 3:3 + N]
+    w = mosaic.Weight(base, packed)
+    flag = mosaic.MQ_GEMM_BASE_ONLY if mode == "base" else mosaic.MQ_GEMM_RESIDUAL_ONLY
+    mosaic.mq_gemv(x, w, y, flag | mosaic.MQ_GEMM_WEIGHTS_READY)
+    W, g = ref.dense_weight(base, packed, mode), float(base["gscale"])
+    want = x.double() @ W.t() * g
+    within(y, want, gemv_bound(x, W, want, g, BF, K), mode)
+    assert (out[:, :3] == 9).all() and (out[:, 3 + N:] == 9).all()
+    first = y.clone()
+    for _ in range(3):
+        mosaic.mq_gemv(x, w, y, flag)
+        assert torch.equal(first, y)
+
+
+@pytest.mark.parametrize("big", [1e-30, 1e30])
+def test_gemv_far_magnitudes(big, dev, mosaic):
+    """bf16 activations far outside fp16's range, and rows of very different size."""
+    N, K, M = 128, 512, 4
+    base, packed = ref.random_weight(N, K, 5, 8, dev)
+    base["gscale"].fill_(2.0 ** -20)
+    x = (torch.randn(M, K, generator=torch.Generator().manual_seed(2)) * torch.tensor([[big], [1.0], [0.0], [big * 7]])).to(BF).to(dev)
+    y = torch.full((M, N), math.nan, dtype=BF, device=dev)
+    mosaic.mq_gemv(x, mosaic.Weight(base, packed), y)
+    W = ref.dense_weight(base, packed)
+    want = x.double() @ W.t() * 2.0 ** -20
+    within(y, want, gemv_bound(x, W, want, 2.0 ** -20, BF, K))
+
+
+def test_gemv_on_a_prepared_layer(dev, mosaic):
+    """The buffers that the layer's own preparation wrote, next to mq_gemm on the same weight."""
+    L = synth.layer("tiny")
+    N, K = L["N"], L["K"]
+    budget = synth.budget_blocks(N, K, 0.10)
+    layer = mosaic.Layer(N, K, budget, dev)
+    layer.prepare_path(to_dev(L["W"], dev), to_dev(L["Xcal"], dev))
+    X = to_dev(L["X"], dev)
+    y = layer.forward_16bit(X)
+    wq = oracle.quantize_weight(L["W"])
+    sel = layer.sel[:budget].cpu().numpy()
+    deq = oracle.nvfp4_dequantize(wq["codes"], wq["sf"], wq["g"]).astype(np.float64)
+    res = oracle.nvfp4_dequantize(wq["r_codes"], wq["r_sf"], wq["g"]).astype(np.float64)
+    mask = np.kron(oracle.block_mask(sel, N, K), np.ones((64, 64)))
+    W = torch.from_numpy(deq + res * mask).to(dev)
+    want = X.double() @ W.t()
+    # the oracle's dequantized values carry one fp32 rounding each (2^-24)
+    within(y, want, gemv_bound(X, W, want, 1.0, BF, K) + 2.0 ** -24 * (X.double().abs() @ W.abs().t()))
+
+
+# ---------------------------------------------------------------------- norms and rotation
+def rope_inputs(T, Hq, Hk, D, dtype, seed, dev, far=131072, theta=1e6, rot=None):
+    gen = torch.Generator().manual_seed(seed)
+    x = (2 * torch.randn(T, Hq + 2 * Hk, D, generator=gen)).to(dtype).to(dev)
+    w = [(1 + 0.3 * torch.randn(D, generator=gen)).to(dtype).to(dev) for _ in range(2)]
+    pos = torch.randint(0, far, (T,), generator=gen).to(dev)
+    rot = D if rot is None else rot
+    freq = (theta ** (-2.0 * torch.arange(rot // 2, dtype=torch.float64) / max(rot, 1))).to(dev)
+    return x[:, :Hq], x[:, Hq:Hq + Hk], x[:, Hq + Hk:], w, pos, freq
+
+
+def rope_bound(want, mag, dtype):
+    """The rounding, and fp32: 16 steps of 2^-24 for the sum of squares and its root, four
+    for the products, 2^-21 for the angle's fp32 fraction (2^-24 of a turn) and its sine."""
+    return ref.rounding(want, dtype) + 2.0 ** -19 * mag
+
+
+@pytest.mark.parametrize("T,Hq,Hk,D,rot,norm,inter", [
+    (1, 1, 1, 64, 64, True, False), (3, 5, 1, 128, 128, True, False), (17, 32, 8, 128, 64, True, True),
+    (5, 7, 7, 256, 256, False, False), (2, 64, 8, 128, 128, False, True), (9, 3, 3, 64, 16, True, False),
+    (4, 6, 2, 128, 96, False, False), (33, 4, 2, 256, 32, True, True), (6, 4, 4, 128, 0, True, False)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_norm_rope(T, Hq, Hk, D, rot, norm, inter, dtype, dev, mosaic):
+    q, k, _, w, pos, freq = rope_inputs(T, Hq, Hk, D, dtype, T * D + rot, dev, rot=rot)
+    wq, wk = w if norm else (None, None)
+    qo, ko = torch.empty_like(q).contiguous(), torch.empty(Hk, T, D, dtype=dtype, device=dev).transpose(0, 1)
+    want = [ref.norm_rope(x, u, 1e-6, pos, freq, rot, inter) for x, u in ((q, wq), (k, wk))]
+    mosaic.mq_qk_norm_rope(q, k, qo, ko, pos, freq if rot else None, wq, wk, 1e-6, inter)
+    for got, (y, mag) in zip((qo, ko), want):
+        within(got, y, rope_bound(y, mag, dtype))
+    # in place, one side at a time: the same bits
+    mosaic.mq_qk_norm_rope(q, None, q, None, pos, freq if rot else None, wq, None, 1e-6, inter)
+    mosaic.mq_qk_norm_rope(None, k, None, k, pos, freq if rot else None, None, wk, 1e-6, inter)
+    assert torch.equal(q, qo) and torch.equal(k, ko)
+
+
+def test_rope_far_positions_and_zero_rows(dev, mosaic):
+    q, k, _, w, pos, freq = rope_inputs(8, 2, 1, 128, HF, 3, dev)
+    pos = torch.tensor([0, 1, -5, 2 ** 20, 2 ** 31, 2 ** 40, -(2 ** 33), 7], device=dev)
+    q[3] = 0
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    mosaic.mq_qk_norm_rope(q, k, qo, ko, pos, freq, w[0], w[1], 1e-6)
+    for got, x, u in ((qo, q, w[0]), (ko, k, w[1])):
+        y, mag = ref.norm_rope(x, u, 1e-6, pos, freq, 128, False)
+        # the angle itself is one fp64 product: 2^-53 of it is unknown to both sides
+        within(got, y, rope_bound(y, mag, HF) + 2.0 ** -52 * pos.abs().double()[:, None, None] * mag)
+    assert (qo[3] == 0).all()
+
+
+# ----------------------------------------------------------------------------- the cache
+def oracle_rows(x, g):
+    """(codes, scales) by the CPU oracle of rows x [T][H][D] with tensor scales g [H]."""
+    T, H, D = x.shape
+    gs = np.ones(T * H, np.float32) if g is None else np.tile(g.cpu().numpy(), T)
+    if T * H == 1:  # one row: the oracle takes a scalar
+        gs = gs[0]
+    r = oracle.nvfp4_quantize(x.float().cpu().numpy().reshape(T * H, D), gs)
+    return r["codes"].reshape(T, H, D // 2), r["sf"].reshape(T, H, D // 16), r["deq"].reshape(T, H, D)
+
+
+@pytest.mark.parametrize("T,H,D,P,pages", [(1, 1, 64, 16, 1), (1, 8, 128, 64, 3), (37, 3, 128, 16, 5), (100, 2, 64, 32, 4),
+                                           (256, 8, 128, 128, 4)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("scales", [True, False])
+def test_append_and_read(T, H, D, P, pages, dtype, scales, dev, mosaic):
+    gen = torch.Generator().manual_seed(T + D)
+    kv = torch.randn(T, 2 * H + 1, D, generator=gen)
+    kv[0, 0, :16] = 0                       # a group of zeros
+    kv[-1, H, :16] = 3000.0                 # one beyond the largest value
+    kv[0, :, 16:32] *= 1e-5                 # one whose scale underflows
+    kv = kv.to(dtype).to(dev)
+    k, v = kv[:, :H], kv[:, H:2 * H]
+    bytes_, ks, vs = ref.random_cache(pages, P, H, D, 1, dev, scales)
+    before = bytes_.clone()
+    cache = mosaic.KVCache(bytes_, ks, vs)
+    slots = torch.randperm(pages * P, generator=gen)[:T].to(dev)
+    mosaic.mq_kv_append(k, v, slots, cache)
+    ko, vo = torch.empty(T, H, D, dtype=dtype, device=dev), torch.empty(T, H, D, dtype=dtype, device=dev)
+    mosaic.mq_kv_read(cache, slots, ko, vo)
+    want = before.cpu().numpy()
+    maps = [m.numpy() for m in ref.record_maps(D, "cpu")]
+    s = slots.cpu().numpy()
+    for x, g, cm, sm, got in ((k, ks, maps[0], maps[2], ko), (v, vs, maps[1], maps[3], vo)):
+        codes, sf, deq = oracle_rows(x, g)
+        for t in range(T):
+            page, rec, i = s[t] // P, s[t] % P // 16, s[t] % 16
+            want[page, :, rec][:, cm[i, ::2]] = codes[t]
+            want[page, :, rec][:, sm[i, ::16]] = sf[t]
+        assert torch.equal(got.cpu(), torch.from_numpy(deq).to(dtype))
+    assert np.array_equal(bytes_.cpu().numpy(), want)  # and nothing beside them
+
+
+def test_append_skips_and_reports(dev, mosaic):
+    H, D, P = 2, 64, 16
+    bytes_, ks, vs = ref.random_cache(2, P, H, D, 4, dev)
+    cache, before = mosaic.KVCache(bytes_, ks, vs), bytes_.clone()
+    k = torch.randn(4, H, D, device=dev).to(BF)
+    slots = torch.tensor([-1, -2 ** 40, -1, -7], device=dev)
+    mosaic.mq_kv_append(k, k, slots, cache)
+    ko, vo = torch.full_like(k, 5.0), torch.full_like(k, 6.0)
+    mosaic.mq_kv_read(cache, slots, ko, vo)
+    assert torch.equal(bytes_, before) and (ko == 5).all() and (vo == 6).all() and mosaic.mq_get_error() == 0
+    # past the cache: left out by the kernels' own checks, and reported
+    for call in (lambda s: mosaic.mq_kv_append(k, k, s, cache), lambda s: mosaic.mq_kv_read(cache, s, ko, vo)):
+        call(torch.tensor([-1, 2 * P, -1, 2 ** 50], device=dev))
+        assert mosaic.mq_get_error() == 1
+        assert torch.equal(bytes_, before) and (ko == 5).all() and (vo == 6).all()
+
+
+@pytest.mark.parametrize("T,Hq,H,D,rot,norm,inter", [(1, 8, 2, 128, 128, True, False), (19, 3, 3, 64, 32, False, True),
+                                                     (64, 64, 8, 128, 128, True, False)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_qkv_append_is_the_two_calls(T, Hq, H, D, rot, norm, inter, dtype, dev, mosaic):
+    q, k, v, w, pos, freq = rope_inputs(T, Hq, H, D, dtype, T, dev, rot=rot)
+    wq, wk = w if norm else (None, None)
+    bytes_, ks, vs = ref.random_cache(8, 16, H, D, 2, dev)
+    slots = torch.randperm(128, generator=torch.Generator().manual_seed(T))[:T].to(dev)
+    slots[T // 2] = -1 if T > 1 else slots[0]
+    a, b, c = (mosaic.KVCache(bytes_.clone(), ks, vs) for _ in range(3))
+    qo, ko, q2, k2 = torch.empty_like(q), torch.empty_like(k), torch.empty_like(q), torch.empty_like(k)
+    mosaic.mq_qk_norm_rope(q, k, qo, ko, pos, freq, wq, wk, 1e-6, inter)
+    mosaic.mq_kv_append(ko, v, slots, a)
+    mosaic.mq_qkv_append(q, k, v, q2, slots, b, pos, freq, wq, wk, 1e-6, inter, k_out=k2)
+    assert torch.equal(qo, q2) and torch.equal(ko, k2) and torch.equal(a.pages, b.pages)
+    mosaic.mq_qkv_append(q, k, v, q, slots, c, pos, freq, wq, wk, 1e-6, inter)  # in place, keys kept in the cache alone
+    assert torch.equal(qo, q) and torch.equal(a.pages, c.pages)
+
+
+# ------------------------------------------------------------------------------ attention
+def attn_inputs(lens, nqs, Hq, H, D, P, dtype, seed, dev, extra_pages=2, qmul=1.0):
+    gen = torch.Generator().manual_seed(seed)
+    per = max(1, -(-max(lens) // P))
+    need = [-(-n // P) for n in lens]
+    pages, ks, vs = ref.random_cache(sum(need) + extra_pages, P, H, D, seed + 1, dev)
+    ids = torch.randperm(sum(need) + extra_pages, generator=gen)
+    table = torch.full((len(lens), per), -1, dtype=torch.int32)  # -1 behind each sequence's pages
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = ids[at:at + n].int()
+        at += n
+    ref.poison(pages, table, lens)
+    T = sum(nqs)
+    q = (qmul * torch.randn(T + 2, Hq + 1, D, generator=gen)).to(dtype).to(dev)[:T, :Hq]
+    cu = torch.tensor([0] + list(np.cumsum(nqs)), dtype=torch.int32, device=dev)
+    return q, pages, ks, vs, table.to(dev), torch.tensor(lens, dtype=torch.int32, device=dev), cu
+
+
+def attn_bounds(out, lse, mass, smax, vmax, dtype, lens):
+    """Scores: D products of an exact fp16 pair in fp32 and one scale: 2^-20 (1 + max |s|)
+    covers them and exp2's 2^-22. The softmax weights enter the second product in fp16 (half
+    a step is 2^-11; below 2^-21 of the row's largest the step is absolute, 2^-32 of it a
+    token), summed in fp32 (n / 8 steps of 2^-24 and 64 for the joins)."""
+    n = max(lens)
+    d = 2.0 ** -20 * (1 + smax)
+    e = mass * (2.0 ** -11 + (n / 8 + 64) * 2.0 ** -24 + 2 * d[..., None]) + n * 2.0 ** -32 * vmax[..., None]
+    return ref.rounding(out.abs() + e, dtype) + e, d + (n / 8 + 64) * 2.0 ** -24 + 2.0 ** -23 * lse.abs().nan_to_num(posinf=0.0)
+
+
+def run_attn(mosaic, q, pages, ks, vs, table, kv_len, cu, max_q, scale, window, dtype, use_cu=True, ws=None):
+    T, Hq, D = q.shape
+    cache = mosaic.KVCache(pages, ks, vs)
+    out = torch.full((T, Hq + 3, D), 77.0, dtype=dtype, device=q.device)
+    o = out[:, 1:1 + Hq]
+    lse = torch.full((T, Hq), 77.0, device=q.device)
+    ws = mosaic.kv_attention_workspace(q, cache, max_q) if ws is None else ws
+    mosaic.mq_kv_attention(q, cache, table, kv_len, o, scale, cu if use_cu else None, max_q, window, lse, ws)
+    assert (out[:, 0] == 77).all() and (out[:, 1 + Hq:] == 77).all()
+    return o, lse
+
+
+CASES = [
+    # lens, query tokens, Hq, H, D, P, window
+    ([1], [1], 1, 1, 64, 16, 0),
+    ([1], [1], 8, 8, 128, 64, 0),
+    ([15, 16, 17, 33], [1] * 4, 8, 2, 128, 16, 0),
+    ([127, 128, 129, 1, 255], [1] * 5, 6, 1, 128, 32, 0),
+    ([0, 5, 300], [1] * 3, 12, 4, 64, 64, 0),
+    ([700, 3], [1] * 2, 64, 8, 128, 128, 0),
+    ([515, 64], [1] * 2, 20, 1, 128, 16, 0),          # 20 query heads on one
+    ([400, 90, 7], [1] * 3, 4, 4, 128, 16, 33),       # a window
+    ([400, 129], [1] * 2, 8, 1, 64, 64, 1),           # a window of one
+    ([40, 3, 200], [5, 3, 1], 8, 2, 128, 32, 0),      # several query tokens
+    ([2, 40], [5, 2], 8, 8, 128, 16, 0),              # more query tokens than cached: rows that see nothing
+    ([0, 0], [2, 1], 4, 2, 64, 16, 0),
+    ([300, 70], [70, 0], 6, 2, 128, 64, 0),           # a whole prompt; a sequence without query tokens
+    ([513], [200], 4, 1, 64, 32, 100),
+    ([260, 31], [130, 31], 8, 1, 128, 16, 17),
+    ([1030] + [9] * 40, [1] * 41, 8, 2, 128, 16, 0),  # one long among many short
+    ([5000], [1], 8, 1, 128, 64, 0),                  # cut into many pieces
+    ([3001, 2999], [3, 4], 16, 2, 64, 16, 0),
+]
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_attention(case, dtype, dev, mosaic):
+    lens, nqs, Hq, H, D, P, window = CASES[case]
+    q, pages, ks, vs, table, kv_len, cu = attn_inputs(lens, nqs, Hq, H, D, P, dtype, case, dev)
+    scale = D ** -0.5
+    want = ref.attention(q, pages, ks, vs, table, lens, nqs, scale, window)
+    one = all(n == 1 for n in nqs)
+    o, lse = run_attn(mosaic, q, pages, ks, vs, table, kv_len, cu, max(nqs), scale, window, dtype, not one)
+    bo, bl = attn_bounds(*want, dtype, lens)
+    within(o, want[0], bo, "out")
+    dead = want[1] == -math.inf
+    assert (lse[dead] == -math.inf).all() and (o[dead] == 0).all()
+    within(lse[~dead], want[1][~dead], bl[~dead], "lse")
+    # the same bits again; a too small expectation of max_q only picks another kernel
+    o2, lse2 = run_attn(mosaic, q, pages, ks, vs, table, kv_len, cu, max(nqs), scale, window, dtype, not one)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    if one:
+        o3, _ = run_attn(mosaic, q, pages, ks, vs, table, kv_len, cu, 1, scale, window, dtype, True)
+        assert torch.equal(o, o3)
+    else:
+        o3, _ = run_attn(mosaic, q, pages, ks, vs, table, kv_len, cu, 1, scale, window, dtype, True)
+        within(o3, want[0], bo, "out, max_q = 1")
+
+
+@pytest.mark.parametrize("qmul,scale", [(60.0, 0.5), (1e-3, 1.0), (1.0, 0.0), (4.0, -0.3)])
+def test_attention_sharp_flat_and_odd_scales(qmul, scale, dev, mosaic):
+    lens, nqs = [777, 64, 1], [2, 1, 1]
+    q, pages, ks, vs, table, kv_len, cu = attn_inputs(lens, nqs, 8, 2, 128, 32, BF, 9, dev, qmul=qmul)
+    want = ref.attention(q, pages, ks, vs, table, lens, nqs, scale, 0)
+    o, lse = run_attn(mosaic, q, pages, ks, vs, table, kv_len, cu, 2, scale, 0, BF)
+    bo, bl = attn_bounds(*want, BF, lens)
+    within(o, want[0], bo, "out")
+    within(lse, want[1], bl, "lse")
+
+
+def test_attention_query_beyond_fp16(dev, mosaic):
+    """bf16 queries far above and below fp16's range, with a scale that brings the scores back."""
+    lens, nqs = [300], [4]
+    q, pages, ks, vs, table, kv_len, cu = attn_inputs(lens, nqs, 8, 2, 128, 32, BF, 10, dev)
+    q = (q.float() * torch.tensor([1e20, 1.0, 1e-20, 1e24], device=dev)[:, None, None]).to(BF)
+    for scale in (1e-21, 1e18):
+        if scale > 1:
+            q[0], q[3], q[1] = 0, 0, 0
+        want = ref.attention(q, pages, ks, vs, table, lens, nqs, scale, 0)
+        o, lse = run_attn(mosaic, q, pages, ks, vs, table, kv_len, cu, 4, scale, 0, BF)
+        bo, bl = attn_bounds(*want, BF, lens)
+        within(o, want[0], bo, "out")
+        within(lse, want[1], bl, "lse")
+
+
+def test_attention_bad_indices_are_reported_and_left_out(dev, mosaic):
+    """Bad pages, lengths and rows meet the kernels' own checks: their tokens are left out."""
+    lens, nqs = [100, 40], [1, 1]
+    q, pages, ks, vs, table, kv_len, cu = attn_inputs(lens, nqs, 8, 2, 128, 16, BF, 21, dev)
+    good = ref.attention(q, pages, ks, vs, table, lens, nqs, 0.1, 0)
+    bound = attn_bounds(*good, BF, lens)[0]
+    for bad in (-1, pages.shape[0], 2 ** 31 - 1):
+        t = table.clone()
+        t[0, 2] = bad
+        o, _ = run_attn(mosaic, q, pages, ks, vs, t, kv_len, cu, 1, 0.1, 0, BF)
+        assert mosaic.mq_get_error() == 1
+        assert torch.isfinite(o).all()
+        within(o[1], good[0][1], bound[1], "the other sequence")
+    for n in (-3, table.shape[1] * 16 + 1, 2 ** 31 - 1):
+        o, lse = run_attn(mosaic, q, pages, ks, vs, table, torch.tensor([n, 40], dtype=torch.int32, device=dev), cu, 1, 0.1, 0, BF)
+        assert mosaic.mq_get_error() == 1
+        assert (o[0] == 0).all() and (lse[0] == -math.inf).all()
+        within(o[1], good[0][1], bound[1], "the other sequence")
+    o, lse = run_attn(mosaic, q, pages, ks, vs, table, kv_len, torch.tensor([0, 1, 9], dtype=torch.int32, device=dev), 1, 0.1, 0, BF)
+    assert mosaic.mq_get_error() == 1  # rows past T
+    within(o[0], good[0][0], bound[0], "the first sequence")
+    assert (o[1] == 77).all()
+
+
+def test_attention_leaves_other_rows(dev, mosaic):
+    lens, nqs = [50, 20], [2, 3]
+    q, pages, ks, vs, table, kv_len, cu = attn_inputs(lens, nqs, 4, 2, 64, 16, HF, 31, dev)
+    q = torch.cat((q, q[:3]))
+    o, lse = run_attn(mosaic, q, pages, ks, vs, table, kv_len, cu, 3, 0.2, 0, HF)
+    assert (o[5:] == 77).all() and (lse[5:] == 77).all() and (o[:5] != 77).any()
+
+
+def test_attention_graphs_and_streams(dev, mosaic):
+    """A captured call replayed with other inputs and lengths, and calls on two streams."""
+    H, D, P, B = 2, 128, 16, 3
+    lens = [200, 31, 90]
+    q, pages, ks, vs, table, kv_len, cu = attn_inputs([256] * B, [1] * B, 8, H, D, P, BF, 41, dev)
+    cache = mosaic.KVCache(pages, ks, vs)
+    kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
+    out, ws = torch.empty_like(q).contiguous(), mosaic.kv_attention_workspace(q, cache, 1)
+    call = lambda w=ws, o=out: mosaic.mq_kv_attention(q, cache, table, kv_len, o, 0.09, ws=w)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for now in (lens, [1, 256, 128], [0, 0, 5]):
+        kv_len.copy_(torch.tensor(now, dtype=torch.int32))
+        q.copy_(torch.randn(q.shape, generator=torch.Generator().manual_seed(sum(now))).to(BF))
+        graph.replay()
+        want = ref.attention(q, pages, ks, vs, table, now, [1] * B, 0.09, 0)
+        within(out, want[0], attn_bounds(*want, BF, [256])[0], str(now))
+    kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
+    call()
+    torch.cuda.synchronize()
+    outs = [torch.empty_like(out) for _ in range(2)]
+    wss = [mosaic.kv_attention_workspace(q, cache, 1) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            mosaic.mq_kv_attention(q, cache, table, kv_len, outs[i], 0.09, ws=wss[i], stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], out) and torch.equal(outs[1], out)
+
+
+# ------------------------------------------------------------------- all of them together
+@pytest.mark.parametrize("norm", [True, False])
+def test_attention_layer(norm, dev, mosaic):
+    """A prompt of 40 tokens (quantized activations), then decode steps of two sequences and a
+    step of three drafted tokens, against the same steps done in 64 bits from the values that
+    the layers, the cache and every rounding hold."""
+    Hq, H, D, hidden, P = 4, 2, 64, 256, 16
+    qkv, out = mosaic.Layer((Hq + 2 * H) * D, hidden, 6, dev), mosaic.Layer(hidden, Hq * D, 4, dev)
+    for i, l in enumerate((qkv, out)):
+        W = to_dev(synth.weight(l.N, l.K, 70 + i, 74, 0.06, 40, 2, 8.0), dev)
+        l.prepare_path(W, to_dev(synth.act(128, l.K, 80 + i, 84, 4, 5.0), dev))
+    cache = mosaic.KVCache.alloc(12, P, H, D, dev)
+    freq = (1e4 ** (-2.0 * torch.arange(D // 2, dtype=torch.float64) / D)).to(dev)
+    gen = torch.Generator().manual_seed(3)
+    w = [(1 + 0.1 * torch.randn(D, generator=gen)).to(BF).to(dev) if norm else None for _ in range(2)]
+    layer = mosaic.AttentionLayer(qkv, out, Hq, cache, freq, w[0], w[1])
+    table = torch.tensor([[3, 7, 1, 0], [5, 2, 9, 4]], dtype=torch.int32, device=dev)
+    lens = [0, 0]
+
+    def step(nqs):
+        T = sum(nqs)
+        X = torch.randn(T, hidden, generator=gen).to(BF).to(dev)
+        pos = torch.cat([lens[b] + torch.arange(n) for b, n in enumerate(nqs)]).to(dev)
+        seq = torch.repeat_interleave(torch.arange(2), torch.tensor(nqs)).to(dev)
+        slots = table[seq, pos // P].long() * P + pos % P
+        for b, n in enumerate(nqs):
+            lens[b] += n
+        cu = torch.tensor([0] + list(np.cumsum(nqs)), dtype=torch.int32, device=dev)
+        kv_len = torch.tensor(lens, dtype=torch.int32, device=dev)
+        y = layer.step(X, pos, slots, table, kv_len, cu, max(nqs)).clone()
+        # the same from the parts: projection, rotation, the cache's own bytes, attention
+        proj = (qkv.forward_16bit(X) if T <= 16 else qkv.forward(X)).clone().view(T, -1, D)
+        qr, mag = ref.norm_rope(proj[:, :Hq], w[0], 1e-6, pos, freq, D, False)
+        kr, _ = ref.norm_rope(proj[:, Hq:Hq + H], w[1], 1e-6, pos, freq, D, False)
+        ko, vo = torch.empty(T, H, D, dtype=BF, device=dev), torch.empty(T, H, D, dtype=BF, device=dev)
+        mosaic.mq_kv_read(cache, slots, ko, vo)
+        for got, src in ((ko, kr), (vo, proj[:, Hq + H:].double())):
+            # a 4-bit value is off by at most 1/4 of its size, or 1/12 of its group's largest
+            g = src.abs().reshape(T, H, -1, 16).amax(-1, keepdim=True).expand(-1, -1, -1, 16).reshape(src.shape)
+            within(got, src, 0.25 * src.abs() + g / 6 * 0.25 * 1.1 + g * 0.07)
+        qb = torch.empty(T, Hq, D, dtype=BF, device=dev)
+        mosaic.mq_qk_norm_rope(proj[:, :Hq], None, qb, None, pos, freq, w[0], None)
+        within(qb, qr, rope_bound(qr, mag, BF))
+        a = ref.attention(qb, cache.pages, None, None, table, lens, nqs, D ** -0.5, 0)
+        o = torch.empty(T, Hq, D, dtype=BF, device=dev)
+        mosaic.mq_kv_attention(qb, cache, table, kv_len, o, D ** -0.5, cu, max(nqs),
+                               ws=mosaic.kv_attention_workspace(qb, cache, max(nqs)))
+        within(o, a[0], attn_bounds(*a, BF, lens)[0], "attention")
+        z = out.forward_16bit(o.view(T, -1)) if T <= 16 else out.forward(o.view(T, -1))
+        assert torch.equal(z, y)
+
+    for nqs in ([23, 17], [1, 1], [1, 1], [3, 1], [0, 2], [9, 1]):
+        step(nqs)

@@ -1,0 +1,163 @@
+"""Host-side checks of the operators of include/mosaic_ops.h: refusals before any launch,
+sizes, and the cache layout's text (each byte of a record used once)."""
+import ctypes
+
+import pytest
+import torch
+
+import ops_ref as ref
+
+
+@pytest.fixture(scope="module")
+def L():
+    from bit_quantized_gemm_zipperengine_b200 import build, mosaic
+    build.build()
+    return mosaic.lib()
+
+
+@pytest.fixture(scope="module")
+def buf():
+    """Real buffers (device memory with a GPU, host memory without, where nothing can launch)."""
+    keep, dev = [], "cuda" if torch.cuda.is_available() else "cpu"
+
+    def make(nbytes, offset=0):
+        t = torch.zeros(nbytes + 256, dtype=torch.uint8, device=dev)
+        keep.append(t)
+        return -(-t.data_ptr() // 128) * 128 + offset
+
+    return make
+
+
+def heads(ptr, n, st, sh):
+    a = (ctypes.c_int64 * 4)(ptr, n, st, sh)
+    return a
+
+
+def test_layout_uses_every_byte_once():
+    for D in (64, 128):
+        used = set()
+        for i in range(16):
+            for d in range(D):
+                kc, vc, ks, vs = ref.record_bytes(i, d, D)
+                used |= {kc, vc, ks, vs}
+        assert used == set(range(18 * D))
+
+
+def test_cache_bytes(L):
+    assert L.mq_kv_cache_bytes(3, 64, 8, 128) == 3 * 64 * 8 * 144
+    assert L.mq_kv_cache_bytes(1 << 20, 128, 8, 128) == (1 << 20) * 128 * 8 * 144  # past 32 bits
+    for bad in ((0, 16, 1, 64), (1, 8, 1, 64), (1, 24, 1, 64), (1, 16, 0, 64), (1, 16, 1, 96), (1, 16, 1, 256)):
+        assert L.mq_kv_cache_bytes(*bad) == 0
+    assert L.mq_kv_attention_workspace_bytes(8, 3, 128, 1) == 0
+    assert L.mq_kv_attention_workspace_bytes(8, 2, 96, 1) == 0
+    assert L.mq_kv_attention_workspace_bytes(8, 2, 128, 0) == 0
+
+
+def test_gemv_refusals(L, buf):
+    from bit_quantized_gemm_zipperengine_b200 import mosaic
+    N, K, M = 128, 256, 4
+    w = mosaic.NVFP4Mat(N, K, buf(N * K // 2), None, buf(N * K // 16), buf(4))
+    r = mosaic.ResidualPacked(N, K, 2, buf(4096), buf(1024), buf(8), buf(12), buf(8))
+    X, Y = buf(17 * K * 2), buf(17 * N * 2)
+
+    def call(X=X, ty=0, ldx=K, w=w, r=None, Y=Y, ldy=N, M=M, N=N, K=K, flags=0):
+        return L.mq_gemv(X, ty, ldx, ctypes.byref(w) if w else None, ctypes.byref(r) if r else None, Y, ldy, M, N, K, flags, None)
+
+    assert call(X=None) == 1 and call(Y=None) == 1 and call(w=None) == 1 and call(ty=2) == 1
+    assert call(M=0) == 1 and call(N=96) == 1 and call(K=96) == 1 and call(N=192) == 1
+    assert call(ldx=K - 8) == 1 and call(ldx=K + 4) == 1 and call(ldy=N - 1) == 1
+    assert call(X=X + 8) == 1 and call(Y=Y + 1) == 1
+    assert call(flags=2) == 1 and call(flags=4 | 8) == 1 and call(flags=16) == 1
+    assert call(M=17) == 2
+    assert call(r=mosaic.ResidualPacked(N, K, 2, buf(4096), buf(1024), None, buf(12), None)) == 1
+    assert call(r=mosaic.ResidualPacked(N, 2 * K, 2, *[getattr(r, f) for f in ("blk_codes", "blk_sf", "blk_kt", "tile_ptr", "bitmap")])) == 1
+    assert call(w=mosaic.NVFP4Mat(N, K, w.codes, None, None, w.gscale)) == 1
+    assert call(w=mosaic.NVFP4Mat(N, K, w.codes + 8, None, w.sf_swz, w.gscale)) == 1
+
+
+def test_rope_and_append_refusals(L, buf):
+    from bit_quantized_gemm_zipperengine_b200 import mosaic
+    T, D = 4, 64
+    mem = buf(1 << 16)
+    h = heads(mem, 2, 2 * D, D)
+    pos, freq, slots = buf(8 * T), buf(8 * D), buf(8 * T)
+
+    def rope(q=h, k=h, qo=h, ko=h, T=T, D=D, ty=0, wq=None, wk=None, eps=1e-6, pos=pos, freq=freq, rot=64):
+        return L.mq_qk_norm_rope(q, k, qo, ko, T, D, ty, wq, wk, eps, pos, freq, rot, 0, None)
+
+    assert rope(q=None) == 1 and rope(k=None) == 1 and rope(q=None, k=None, qo=None, ko=None) == 1
+    assert rope(T=-1) == 1 and rope(D=96) == 1 and rope(ty=7) == 1
+    assert rope(rot=72) == 1 and rope(rot=80) == 1 and rope(rot=-16) == 1 and rope(pos=None) == 1 and rope(freq=None) == 1
+    assert rope(eps=-1.0) == 1 and rope(eps=float("nan")) == 1 and rope(wq=mem + 2) == 1
+    for bad in (heads(mem + 2, 2, 2 * D, D), heads(mem, 2, 2 * D + 4, D), heads(mem, 2, 2 * D, D + 4), heads(mem, 0, 2 * D, D),
+                heads(mem, 2, -2 * D, D), heads(0, 2, 2 * D, D)):
+        assert rope(q=bad) == 1 and rope(qo=bad) == 1
+    assert rope(qo=heads(mem, 2, 2 * D, 0)) == 1 and rope(qo=heads(mem, 2, 0, D)) == 1  # rows that overlap
+    assert rope(qo=heads(mem, 3, 3 * D, D)) == 1                                        # other heads than q's
+    assert rope(T=0, q=heads(0, 2, 0, 0), k=None, qo=heads(0, 2, 0, 0), ko=None) == 0   # nothing to do
+
+    pages = buf(4 * 2 * 2 * 1152)
+    c = mosaic.KVCacheStruct(pages, 4, 32, 2, 64, None, None)
+
+    def app(k=h, v=h, T=T, ty=0, slots=slots, c=c):
+        return L.mq_kv_append(k, v, T, ty, slots, ctypes.byref(c) if c else None, None)
+
+    def read(k=h, v=h, T=T, ty=0, slots=slots, c=c):
+        return L.mq_kv_read(ctypes.byref(c) if c else None, slots, T, k, v, ty, None)
+
+    for f in (app, read):
+        assert f(k=None) == 1 and f(v=None) == 1 and f(T=-2) == 1 and f(ty=-1) == 1 and f(slots=None) == 1 and f(c=None) == 1
+        assert f(k=heads(mem, 3, 3 * D, D)) == 1 and f(v=heads(mem, 1, D, D)) == 1
+        for bad in ((pages, 4, 24, 2, 64), (pages, 0, 32, 2, 64), (pages + 64, 4, 32, 2, 64), (None, 4, 32, 2, 64), (pages, 4, 32, 2, 256)):
+            assert f(c=mosaic.KVCacheStruct(*bad, None, None)) == 1
+        assert f(T=0) == 0
+    assert read(k=heads(mem, 2, 2 * D, 0)) == 1
+
+    def both(q=h, k=h, v=h, qo=h, ko=None, slots=slots, c=c, rot=64):
+        return L.mq_qkv_append(q, k, v, qo, ko, T, 0, None, None, 1e-6, pos, freq, rot, 0, slots, ctypes.byref(c), None)
+
+    assert both(q=None) == 1 and both(k=None) == 1 and both(v=None) == 1 and both(qo=None) == 1 and both(slots=None) == 1
+    assert both(rot=24) == 1 and both(k=heads(mem, 1, D, D)) == 1 and both(ko=heads(mem, 1, D, D)) == 1
+
+
+def test_attention_refusals(L, buf):
+    from bit_quantized_gemm_zipperengine_b200 import mosaic
+    T, D, B = 3, 64, 3
+    q, o = heads(buf(1 << 14), 4, 4 * D, D), heads(buf(1 << 14), 4, 4 * D, D)
+    c = mosaic.KVCacheStruct(buf(4 * 2 * 2 * 1152), 4, 32, 2, 64, None, None)
+    table, lens, cu = buf(4 * B * 4), buf(4 * B), buf(16)
+    n = L.mq_kv_attention_workspace_bytes(4, 2, 64, 1)
+    ws = buf(max(n, 16))
+
+    def call(q=q, o=o, T=T, ty=0, c=c, table=table, stride=4, pages=4, B=B, cu=cu, mq=1, lens=lens, scale=0.1, window=0, ws=ws, n=n):
+        return L.mq_kv_attention(q, o, None, T, ty, ctypes.byref(c) if c else None, table, stride, pages, B, cu, mq, lens, scale, window,
+                                 ws, n, None)
+
+    assert call(q=None) == 1 and call(o=None) == 1 and call(c=None) == 1 and call(table=None) == 1 and call(lens=None) == 1
+    assert call(T=-1) == 1 and call(B=-1) == 1 and call(ty=2) == 1 and call(mq=0) == 1 and call(window=-1) == 1
+    assert call(scale=float("inf")) == 1 and call(scale=float("nan")) == 1
+    assert call(stride=3) == 1 and call(pages=0) == 1 and call(cu=None, B=2) == 1
+    assert call(q=heads(q[0], 3, 3 * D, D), o=heads(o[0], 3, 3 * D, D)) == 1
+    assert call(o=q) == 1 and call(o=heads(o[0], 4, 4 * D, 0)) == 1 and call(o=heads(o[0], 2, 4 * D, D)) == 1
+    if n:
+        assert call(ws=None) == 3 and call(n=n - 1) == 3 and call(ws=ws + 8) == 3
+    assert call(T=0) == 0 and call(B=0) == 0
+
+
+def test_binding_refuses_cpu_tensors_and_wrong_types():
+    from bit_quantized_gemm_zipperengine_b200 import mosaic
+    pages = torch.zeros(2, 2, 1, 1152, dtype=torch.uint8)
+    with pytest.raises(mosaic.MosaicError):
+        mosaic.KVCache(pages)                              # a CPU tensor
+    with pytest.raises(mosaic.MosaicError):
+        mosaic.KVCache(pages.float())
+    with pytest.raises(mosaic.MosaicError):
+        mosaic.KVCache.alloc(2, 24, 2, 64, "cpu")
+    x = torch.zeros(2, 2, 64)
+    with pytest.raises(mosaic.MosaicError):                # fp32
+        mosaic.mq_qk_norm_rope(x, None, x, None)
+    y = x.to(torch.bfloat16)
+    with pytest.raises(mosaic.MosaicError):                # two types
+        mosaic.mq_qk_norm_rope(y, None, x.to(torch.float16), None)
+    with pytest.raises(mosaic.MosaicError):                # a CPU tensor
+        mosaic.mq_qk_norm_rope(y, None, y, None)
