@@ -1802,7 +1802,7 @@ cudaError_t launch_gemm_decode(const CUtensorMap& tw, const CUtensorMap& tx, Gem
     }
 }
 
-static int device_sms() {
+int device_sms() {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) !=
                                                    cudaSuccess || sms <= 0) {

@@ -110,6 +110,7 @@ struct AttnParams {
 // api.cu: a launch's status, counted in mq_launch_count; the current device's error word
 mq_status count_launches(cudaError_t e, int kernels);
 int* device_error_word();
+int device_sms();  // gemm.cu: SMs of the current device (148 without one)
 
 cudaError_t launch_heads(const HeadsParams& p, int D, bool f16, cudaStream_t s);
 cudaError_t launch_kv_read(const HeadsParams& p, int D, bool f16, cudaStream_t s);
