@@ -24,6 +24,7 @@
 // equal share, wherever the sequences end. Runs that a share boundary cuts leave partial
 // sums in the workspace; whoever finishes a run last adds its parts in their order, so the
 // result does not depend on the timing.
+#include <cfloat>
 #include <climits>
 
 #include "ops.cuh"
@@ -139,8 +140,19 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v) {
     return v;
 }
 
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+// ln of the sum of 2^z, kept as sum = sum of 2^(z - top + kShift).
+__device__ __forceinline__ float lse_of(float top, float sum) {
+    return sum > 0.0f ? (top - kShift + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+}
+
 template <int D, int NT, bool F16>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const AttnParams p) {
+    constexpr bool PAIR = NT == 1;
     constexpr int R = 8 * NT;           // rows of a tile
     constexpr int REC = 18 * D;         // bytes of a record
     constexpr int KS = D / 16;          // products of 16 d per token tile; also d tiles of the output
@@ -159,8 +171,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
     griddep_launch();
 
     // total units, then the sequence that holds this CTA's first one
-    int64_t mine = 0;
-    for (int b = tid; b < p.B; b += kThreads) mine += seq_units(seq_of(p, b, blockIdx.x == 0), G, p.window, R) * H;
+    const int64_t own = tid < p.B ? seq_units(seq_of(p, tid, blockIdx.x == 0), G, p.window, R) * H : 0;
+    int64_t mine = own;
+    for (int b = tid + kThreads; b < p.B; b += kThreads)
+        mine += seq_units(seq_of(p, b, blockIdx.x == 0), G, p.window, R) * H;
     mine = warp_sum(mine);
     if (lane == 0) red[warp] = mine;
     __syncthreads();
@@ -175,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
         int64_t base = 0;
         for (int b0 = 0; b0 < p.B; b0 += kThreads) {
             const int b = b0 + tid;
-            const int64_t n = b < p.B ? seq_units(seq_of(p, b, false), G, p.window, R) * H : 0;
+            const int64_t n = b0 == 0 ? own : b < p.B ? seq_units(seq_of(p, b, false), G, p.window, R) * H : 0;
             int64_t x = n;  // inclusive scan over the CTA
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -220,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
 
     uint8_t* ring = smem + warp * (kStages * 2 * REC);
     float* merge = reinterpret_cast<float*>(smem);
-    uint32_t it = 0;    // steps this warp has taken from its ring
+    uint32_t at = 0, phase = 0;  // ring place and parity of this warp's next step
     bool alive = true;  // false after a wait that gave up
     int64_t u = u0;
     while (true) {
@@ -232,30 +246,34 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
         const float gk = p.cache.k_scale ? __ldg(p.cache.k_scale + h) : 1.0f;
         const float gv = p.cache.v_scale ? __ldg(p.cache.v_scale + h) : 1.0f;
 
-        // issue the step-th step of this warp: lane 0 and 1 fetch a record each
+        // this warp's steps, and their copies: two records each
         const int first = begin + piece * kUnit + warp * kStep;
         const int steps = first < end ? min(take, (end - first + kUnit - 1) / kUnit) : 0;
-        uint32_t bad = 0;  // bits 2 i, 2 i + 1: record 0 or 1 of the step in ring place i is not there
+        uint32_t bad = 0;           // bits 2 i, 2 i + 1: record 0 or 1 of the step in ring place i is not there
+        uint32_t to = at;           // ring place of the next issue
+        const uint8_t* src = nullptr;  // lane 2 i + r: record r of step 16 k + i (null: not there), 16 steps at a time
         auto issue = [&](int step) {
-            const uint32_t at = (it + step) % kStages;
-            bool ok = false;
-            const uint8_t* src = nullptr;
-            if (lane < 2) {
-                const int j = first + step * kUnit + 16 * lane;
+            if ((step & 15) == 0) {
+                const int j = first + (step + (lane >> 1)) * kUnit + 16 * (lane & 1);
+                src = nullptr;
                 if (j < end) {
                     const int pg = j / p.cache.page_size;
                     const int page = __ldg(p.table + b * p.table_stride + pg);
-                    ok = page >= 0 && page < p.cache.num_pages;
-                    if (!ok) report_index(p.err);
-                    src = p.cache.pages + (((int64_t)page * H + h) * (p.cache.page_size >> 4) + ((j - pg * p.cache.page_size) >> 4)) * REC;
+                    if (page >= 0 && page < p.cache.num_pages)
+                        src = p.cache.pages +
+                              (((int64_t)page * H + h) * (p.cache.page_size >> 4) + ((j - pg * p.cache.page_size) >> 4)) * REC;
+                    else if (step + (lane >> 1) < steps)
+                        report_index(p.err);
                 }
             }
-            const uint32_t have = __ballot_sync(0xffffffffu, ok) & 3u;
-            bad = (bad & ~(3u << (2 * at))) | ((~have & 3u) << (2 * at));
-            uint64_t* bar = &full[warp][at];
+            const int turn = step & 15;
+            const uint32_t have = (__ballot_sync(0xffffffffu, src != nullptr) >> (2 * turn)) & 3u;
+            bad = (bad & ~(3u << (2 * to))) | ((~have & 3u) << (2 * to));
+            uint64_t* bar = &full[warp][to];
             if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)__popc(have) * REC);
             __syncwarp();
-            if (ok) bulk_load(ring + at * (2 * REC) + lane * REC, src, REC, bar);
+            if ((lane >> 1) == turn && src) bulk_load(ring + to * (2 * REC) + (lane & 1) * REC, src, REC, bar);
+            to = to + 1 == kStages ? 0 : to + 1;
         };
 #pragma unroll
         for (int i = 0; i < kStages; ++i)
@@ -266,7 +284,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
         uint32_t qf[NT][KS][2];
         float qs[NT][2];
         int lim[NT][2];
-        float m[NT][2], l[NT][2], o[KS][NT][4];
+        float m[NT][2], l[NT][2];
+        float ref[NT][2];    // m - kShift (0 while m is -inf)
+        float limit[NT][2];  // the unscaled score that raises m
+        // outputs: with PAIR, o[2 i + e] holds elements e of the d pairs 2 i, 2 i + 1
+        float o[KS][NT][4];
         int lim_min = INT_MAX;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -287,6 +309,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
                     qf[nt][2 * i + 1][1] = v.w;
                 }
                 inv = 1.0f;
+                if (F16 && p.scale < 0.0f)  // the sign of the scale goes into the query: qs > 0
+#pragma unroll
+                    for (int j = 0; j < KS; ++j) qf[nt][j][0] ^= 0x80008000u, qf[nt][j][1] ^= 0x80008000u;
             }
             if constexpr (!F16) {
                 float top = 0.0f;
@@ -301,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 // the largest element to [2^14, 2^15)
                 const uint32_t ex = max(__float_as_uint(top) >> 23, 15u);
-                const float up = __uint_as_float((268u - ex) << 23);
+                const float up = copysignf(__uint_as_float((268u - ex) << 23), p.scale);
                 inv *= __uint_as_float((ex - 14u) << 23);
 #pragma unroll
                 for (int j = 0; j < KS; ++j)
@@ -311,7 +336,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
                         qf[nt][j][i] = narrow2<true>(f.x * up, f.y * up);
                     }
             }
-            const float z = inv * gk * p.scale;
+            // never zero: a masked score is -inf before the scale (with this least scale every
+            // other score rounds to 0)
+            const float z = fmaxf(inv * gk * fabsf(p.scale), FLT_MIN);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 qs[nt][c] = __shfl_sync(0xffffffffu, z, 4 * (2 * t + c));
@@ -319,6 +346,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
                 lim[nt][c] = r < rows ? s.len - s.nq + r / G + 1 : INT_MAX;
                 lim_min = min(lim_min, lim[nt][c]);
                 m[nt][c] = -INFINITY;
+                ref[nt][c] = 0.0f;
+                limit[nt][c] = -INFINITY;
                 l[nt][c] = 0.0f;
             }
         }
@@ -335,13 +364,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
         const int lo_min = p.window > 0 ? s.len - s.nq + r0 / G + 1 - p.window : 0;
 
         for (int step = 0; step < steps && alive; ++step) {
-            const uint32_t at = (it + step) % kStages;
-            if (!mbar_wait_err(&full[warp][at], ((it + step) / kStages) & 1u, p.err)) alive = false;
-            alive = __all_sync(0xffffffffu, alive);
-            if (!alive) {
+            if (!mbar_wait_err(&full[warp][at], phase, p.err)) alive = false;
+            if (!__all_sync(0xffffffffu, alive)) {
                 // give the copies behind it their (bounded) time, then leave
-                for (int i = step + 1; i < min(steps, step + kStages); ++i)
-                    mbar_wait_err(&full[warp][(it + i) % kStages], ((it + i) / kStages) & 1u, p.err);
+                alive = false;
+                for (int i = 1; i < min(steps - step, kStages); ++i) {
+                    const uint32_t x = at + i;
+                    mbar_wait_err(&full[warp][x % kStages], phase ^ (x >= kStages), p.err);
+                }
                 break;
             }
             const uint8_t* buf = ring + at * (2 * REC);
@@ -393,10 +423,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
                         for (int nt = 0; nt < NT; ++nt) mma_f16(z[r][nt], a, qf[nt][2 * w + i][0], qf[nt][2 * w + i][1]);
                     }
                 }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) z[r][nt][c] *= qs[nt][c & 1];
             }
             if (!whole) {
 #pragma unroll
@@ -417,18 +443,20 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
-                    rise |= fmaxf(fmaxf(z[0][nt][c], z[0][nt][c + 2]), fmaxf(z[1][nt][c], z[1][nt][c + 2])) > m[nt][c] + kSlack;
+                    rise |= fmaxf(max3(z[0][nt][c], z[0][nt][c + 2], z[1][nt][c]), z[1][nt][c + 2]) > limit[nt][c];
             if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        float top = fmaxf(fmaxf(z[0][nt][c], z[0][nt][c + 2]), fmaxf(z[1][nt][c], z[1][nt][c + 2]));
+                        float top = fmaxf(max3(z[0][nt][c], z[0][nt][c + 2], z[1][nt][c]), z[1][nt][c + 2]);
 #pragma unroll
                         for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                        const float mn = fmaxf(m[nt][c], top);
+                        const float mn = fmaxf(m[nt][c], top * qs[nt][c]);
                         const float f = mn == -INFINITY ? 1.0f : ex2(m[nt][c] - mn);
                         m[nt][c] = mn;
+                        ref[nt][c] = mn == -INFINITY ? 0.0f : mn - kShift;
+                        limit[nt][c] = (mn + kSlack) / qs[nt][c];
                         l[nt][c] *= f;
 #pragma unroll
                         for (int j = 0; j < KS; ++j) {
@@ -445,8 +473,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
                     float w[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const float ref = m[nt][c & 1] == -INFINITY ? 0.0f : m[nt][c & 1] - kShift;
-                        w[c] = ex2(z[r][nt][c] - ref);
+                        w[c] = ex2(__fmaf_rn(z[r][nt][c], qs[nt][c & 1], -ref[nt][c & 1]));
                         l[nt][c & 1] += w[c];
                     }
                     pb[r][nt][0] = transpose8x8(narrow2<true>(w[0], w[1]));
@@ -498,6 +525,23 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
 #pragma unroll
                         for (int e = 0; e < 4; ++e) x[i][e] = mul_h2(x[i][e], f[i]);
                     }
+                    if constexpr (PAIR) {
+                        // the product's k pair is the two d of a byte, its row a byte: against (p, 0)
+                        // it sums the even d, against (0, p) the odd ones, eight tokens a product
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {  // tokens 0..7, 8..15
+                                const uint32_t a[4] = {x[2 * e][2 * i], x[2 * e][2 * i + 1], x[2 * e + 1][2 * i],
+                                                       x[2 * e + 1][2 * i + 1]};
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    const uint32_t pr = pb[r][nt][e];
+                                    mma_f16(o[2 * (2 * w + i)][nt], a, pr & 0xFFFFu, pr >> 16);
+                                    mma_f16(o[2 * (2 * w + i) + 1][nt], a, pr << 16, pr & 0xFFFF0000u);
+                                }
+                            }
+                    } else
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const uint32_t a[4] = {__byte_perm(x[0][e], x[1][e], 0x5410), __byte_perm(x[0][e], x[1][e], 0x7632),
@@ -509,11 +553,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
             }
             __syncwarp();
             if (step + kStages < steps) issue(step + kStages);
+            if (++at == kStages) at = 0, phase ^= 1u;
         }
-        it += steps;
 
         // ---------------------------------------------------------------- join the warps
-        // d of o[j][.][c]: g D/8 + 2 j + (c >> 1). A merged row lies as [j][g][2], RS floats.
+        // Without PAIR, o[j][.][c] is d = g D/8 + 2 j + (c >> 1). A merged row lies as [j][g][2] (d = g D/8 + 2 j + .), RS floats.
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -540,7 +584,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
                 const float f = m[nt][c] == -INFINITY ? 0.0f : ex2(m[nt][c] - top);
                 float2* dst = reinterpret_cast<float2*>(merge + (warp * R + row) * RS) + g;
 #pragma unroll
-                for (int j = 0; j < KS; ++j) dst[8 * j] = make_float2(o[j][nt][c] * f, o[j][nt][c + 2] * f);
+                for (int j = 0; j < KS; ++j)
+                    dst[8 * j] = PAIR ? make_float2(o[j & ~1][nt][c + 2 * (j & 1)] * f, o[j | 1][nt][c + 2 * (j & 1)] * f)
+                                      : make_float2(o[j][nt][c] * f, o[j][nt][c + 2] * f);
             }
         __syncthreads();
         const int rows = min(R, s.nq * G - r0);
@@ -583,40 +629,78 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
             __syncthreads();
             if (last_part) __threadfence();
         }
-        if (parts == 1 || last_part) {
+        if (parts == 1) {
             for (int row = tid / PAIRS; row < rows; row += RPP) {
                 float2 a = make_float2(0.0f, 0.0f);
-                float top = -INFINITY, sum = 0.0f;
-                if (parts == 1) {
+                float top = sm_m[0][row], sum = 0.0f;
 #pragma unroll
-                    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm_m[w][row]);
+                for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm_m[w][row]);
 #pragma unroll
-                    for (int w = 0; w < kWarps; ++w) {
-                        const float2 v = reinterpret_cast<const float2*>(merge + (w * R + row) * RS)[8 * pj + pg];
-                        a.x += v.x;
-                        a.y += v.y;
-                        sum += sm_m[w][row] == -INFINITY ? 0.0f : sm_l[w][row] * ex2(sm_m[w][row] - top);
-                    }
-                } else {
-                    for (int64_t w = w_first; w <= w_last; ++w) {
-                        const float* src = p.partial + (2 * w + (w == w_first && run >= w * share ? 1 : 0)) * slot_floats(NT, D);
-                        top = fmaxf(top, __ldcg(src + R * D + row));
-                    }
-                    for (int64_t w = w_first; w <= w_last; ++w) {
-                        const float* src = p.partial + (2 * w + (w == w_first && run >= w * share ? 1 : 0)) * slot_floats(NT, D);
-                        const float mw = __ldcg(src + R * D + row), f = mw == -INFINITY ? 0.0f : ex2(mw - top);
-                        const float2 v = __ldcg(reinterpret_cast<const float2*>(src + row * D) + pi);
-                        a.x = __fmaf_rn(v.x, f, a.x);
-                        a.y = __fmaf_rn(v.y, f, a.y);
-                        sum = __fmaf_rn(__ldcg(src + R * D + R + row), f, sum);
-                    }
+                for (int w = 0; w < kWarps; ++w) {
+                    const float2 v = reinterpret_cast<const float2*>(merge + (w * R + row) * RS)[8 * pj + pg];
+                    a.x += v.x;
+                    a.y += v.y;
+                    sum += sm_m[w][row] == -INFINITY ? 0.0f : sm_l[w][row] * ex2(sm_m[w][row] - top);
                 }
                 const int qi = (r0 + row) / G, hq = h * G + r0 + row - qi * G;
                 const int64_t tok = s.row0 + qi;
                 const float inv = sum > 0.0f ? gv / sum : 0.0f;
                 *reinterpret_cast<uint32_t*>(p.o.p + tok * p.o.st + hq * p.o.sh + 2 * pi) = narrow2<F16>(a.x * inv, a.y * inv);
-                if (p.lse && pi == 0)
-                    p.lse[tok * p.q.heads + hq] = sum > 0.0f ? (top - kShift + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+                if (p.lse && pi == 0) p.lse[tok * p.q.heads + hq] = lse_of(top, sum);
+            }
+        } else if (last_part) {
+            // part 0 lies in its CTA's slot 1, the others in their CTAs' slots 0. A warp takes a
+            // row's maxima and sums and leaves the parts' factors in shared memory; then all
+            // threads add the rows, four elements each.
+            constexpr int SLOT = slot_floats(NT, D), QUADS = D / 4;
+            const float* part0 = p.partial + (2 * w_first + 1) * SLOT;
+            const float* parts1 = p.partial + 2 * w_first * SLOT;  // part i > 0 at + 2 i SLOT
+            float* fac = merge;                                    // [parts][R]: the merge's rows are not needed any more
+            for (int row = warp; row < rows; row += kWarps) {
+                float top = -INFINITY, sum = 0.0f;
+                for (int i = lane; i < parts; i += 32)
+                    top = fmaxf(top, __ldcg((i ? parts1 + (int64_t)2 * i * SLOT : part0) + R * D + row));
+                top = warp_max(top);
+                for (int i = lane; i < parts; i += 32) {
+                    const float* src = (i ? parts1 + (int64_t)2 * i * SLOT : part0) + R * D + row;
+                    const float mw = __ldcg(src), f = mw == -INFINITY ? 0.0f : ex2(mw - top);
+                    fac[i * R + row] = f;
+                    sum = __fmaf_rn(__ldcg(src + R), f, sum);
+                }
+#pragma unroll
+                for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                if (lane == 0) {
+                    sm_l[0][row] = sum;
+                    sm_m[0][row] = top;
+                }
+            }
+            __syncthreads();
+            for (int i = tid; i < rows * QUADS; i += kThreads) {
+                const int row = i / QUADS, d = 4 * (i - row * QUADS);
+                float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                auto add = [&](const float4& v, float f) {
+                    a.x = __fmaf_rn(v.x, f, a.x);
+                    a.y = __fmaf_rn(v.y, f, a.y);
+                    a.z = __fmaf_rn(v.z, f, a.z);
+                    a.w = __fmaf_rn(v.w, f, a.w);
+                };
+                add(__ldcg(reinterpret_cast<const float4*>(part0 + row * D + d)), fac[row]);
+                const float* src = parts1 + row * D + d;
+                int w = 1;
+                for (; w + 8 <= parts; w += 8) {
+                    float4 v[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) v[x] = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)2 * (w + x) * SLOT));
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) add(v[x], fac[(w + x) * R + row]);
+                }
+                for (; w < parts; ++w) add(__ldcg(reinterpret_cast<const float4*>(src + (int64_t)2 * w * SLOT)), fac[w * R + row]);
+                const int qi = (r0 + row) / G, hq = h * G + r0 + row - qi * G;
+                const int64_t tok = s.row0 + qi;
+                const float sum = sm_l[0][row], inv = sum > 0.0f ? gv / sum : 0.0f;
+                *reinterpret_cast<uint2*>(p.o.p + tok * p.o.st + hq * p.o.sh + d) =
+                    make_uint2(narrow2<F16>(a.x * inv, a.y * inv), narrow2<F16>(a.z * inv, a.w * inv));
+                if (p.lse && d == 0) p.lse[tok * p.q.heads + hq] = lse_of(sm_m[0][row], sum);
             }
         }
         // ---------------------------------------------------------------- the next run
