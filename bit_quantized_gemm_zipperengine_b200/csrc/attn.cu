@@ -19,11 +19,11 @@
 // when a score passes it by 8 (one vote a step, no shuffles), so p stays under 2^15 and its
 // fp16 copy keeps all 11 bits down to 2^-21 of the largest. Sums and outputs are fp32.
 //
-// Work split: every (sequence, cache head, tile of rows) is a run of 128-token units; the
-// units of all runs are numbered through, and CTA w of a grid that just fills the GPU takes the w-th
-// equal share, wherever the sequences end. Runs that a share boundary cuts leave partial
-// sums in the workspace; whoever finishes a run last adds its parts in their order, so the
-// result does not depend on the timing.
+// Work split: every (sequence, cache head, tile of rows) is a run of 128-token units. The grid
+// just fills the GPU, and the runs are cut so that every CTA has about the same number of
+// units, wherever the sequences end. Runs that are cut leave partial sums in the workspace;
+// whoever finishes a run last adds its parts in their order, so the result does not depend on
+// the timing.
 #include <cfloat>
 #include <climits>
 
@@ -37,7 +37,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 32;               // tokens a warp takes at a time
 constexpr int kUnit = kStep * kWarps;   // tokens of a unit
-constexpr int kStages = 3;              // steps in flight per warp
+constexpr int kStages = 2;              // steps in flight per warp (a power of two)
+constexpr int kJoin = 4;                // what a second run costs a CTA, in units
 constexpr float kShift = 7.0f;          // exponent offset of the fp16 softmax weights
 constexpr float kSlack = 8.0f;          // how far a score may pass its row's reference
 
@@ -51,6 +52,11 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 // Transpose of an 8 x 8 matrix of 16-bit elements held by the warp.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -83,13 +89,11 @@ __device__ __forceinline__ void e4m3x4_half(uint32_t w, uint32_t& lo, uint32_t& 
         : "=r"(lo), "=r"(hi)
         : "r"(w));
 }
-__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-__device__ __forceinline__ uint32_t low2(uint32_t a) { return __byte_perm(a, a, 0x1010); }
-__device__ __forceinline__ uint32_t high2(uint32_t a) { return __byte_perm(a, a, 0x3232); }
+__device__ __forceinline__ __half2 as_h2(uint32_t a) { return *reinterpret_cast<const __half2*>(&a); }
+__device__ __forceinline__ uint32_t as_u32(__half2 a) { return *reinterpret_cast<const uint32_t*>(&a); }
+__device__ __forceinline__ uint32_t mul_h2(uint32_t a, __half2 b) { return as_u32(__hmul2(as_h2(a), b)); }
+__device__ __forceinline__ __half2 low2(uint32_t a) { return __low2half2(as_h2(a)); }
+__device__ __forceinline__ __half2 high2(uint32_t a) { return __high2half2(as_h2(a)); }
 
 // Sequence b: its rows of q and its length, checked.
 struct Seq {
@@ -134,6 +138,14 @@ __device__ __forceinline__ int64_t seq_units(const Seq& s, int G, int window, in
     return n;
 }
 
+// A CTA's part of one run of units: (sequence, cache head, tile of rows), pieces [piece,
+// piece + take) of its `units`, its first unit's number, and its tokens.
+struct Run {
+    Seq s;
+    int b, h, r0, piece, units, take, begin, end;
+    int64_t unit0;
+};
+
 __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -152,7 +164,6 @@ __device__ __forceinline__ float lse_of(float top, float sum) {
 
 template <int D, int NT, bool F16>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const AttnParams p) {
-    constexpr bool PAIR = NT == 1;
     constexpr int R = 8 * NT;           // rows of a tile
     constexpr int REC = 18 * D;         // bytes of a record
     constexpr int KS = D / 16;          // products of 16 d per token tile; also d tiles of the output
@@ -160,36 +171,74 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t full[kWarps][kStages];
     __shared__ float sm_m[kWarps][R], sm_l[kWarps][R];
-    __shared__ int64_t red[kWarps];
+    __shared__ int64_t red[kWarps], red2[kWarps];
     __shared__ int64_t found[4];
     __shared__ int last_part;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int H = p.cache.heads, G = p.q.heads / H;
-    if (tid < kWarps * kStages) mbar_init(&full[0][0] + tid, 1);
+    if (tid < kWarps * kStages) mbar_init(&full[0][0] + tid, 2);  // the two records' lanes
     mbar_fence_init();
     griddep_wait();
     griddep_launch();
 
-    // total units, then the sequence that holds this CTA's first one
-    const int64_t own = tid < p.B ? seq_units(seq_of(p, tid, blockIdx.x == 0), G, p.window, R) * H : 0;
-    int64_t mine = own;
-    for (int b = tid + kThreads; b < p.B; b += kThreads)
-        mine += seq_units(seq_of(p, b, blockIdx.x == 0), G, p.window, R) * H;
+    // The CTA's work. CTA w takes the w-th equal share of all units, in order; or, with fewer
+    // runs than CTAs, every run is cut into equal pieces of at most q units, one CTA each, q the
+    // least for which the CTAs suffice. Then no CTA joins two runs, which costs it about as
+    // much as kJoin units (16 sequences of up to 8192 tokens: 33.2 us by shares, 31.8 by pieces;
+    // 4 of 131072, where pieces waste 5 of 74 units: 126.6 and 132.7).
+    const Seq own = tid < p.B ? seq_of(p, tid, blockIdx.x == 0) : Seq{0, 0, 0};
+    const int64_t own_units = seq_units(own, G, p.window, R) * H;
+    int64_t mine = own_units, rmine = (int64_t)((own.nq * G + R - 1) / R) * H;
+    for (int b = tid + kThreads; b < p.B; b += kThreads) {
+        const Seq s = seq_of(p, b, blockIdx.x == 0);
+        mine += seq_units(s, G, p.window, R) * H;
+        rmine += (int64_t)((s.nq * G + R - 1) / R) * H;
+    }
     mine = warp_sum(mine);
-    if (lane == 0) red[warp] = mine;
+    rmine = warp_sum(rmine);
+    if (lane == 0) {
+        red[warp] = mine;
+        red2[warp] = rmine;
+    }
+    if (tid == 0) found[0] = -1;
     __syncthreads();
-    int64_t total = 0;
+    int64_t total = 0, runs = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += red[w];
+    for (int w = 0; w < kWarps; ++w) {
+        total += red[w];
+        runs += red2[w];
+    }
     if (total == 0) return;
-    const int64_t share = (total + gridDim.x - 1) / gridDim.x;
-    const int64_t u0 = share * blockIdx.x, u1 = min(u0 + share, total);
-    if (u0 >= u1) return;
+    const int grid = (int)gridDim.x;
+    const bool fits = total < (1 << 30);  // 32-bit divisions
+    const int64_t share = fits ? ((int)total + grid - 1) / grid : (total + grid - 1) / grid;
+    auto pieces_of = [&](const Seq& s, int q) {  // of one cache head
+        int n = 0;
+        for (int r0 = 0; r0 < s.nq * G; r0 += R) n += (units_of(s, G, p.window, r0, R) + q - 1) / q;
+        return n;
+    };
+    bool cut = false;
+    int q = (int)share;
+    if (fits && p.B <= kThreads && runs < grid) {
+        for (; q <= (int)share + kJoin && !cut; q += !cut) {
+            const int n = __reduce_add_sync(0xffffffffu, pieces_of(own, q) * H);
+            __syncthreads();
+            if (lane == 0) red[warp] = n;
+            __syncthreads();
+            int sum = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) sum += (int)red[w];
+            cut = sum <= grid;
+        }
+    }
+    const int64_t at0 = cut ? blockIdx.x : share * blockIdx.x;  // the CTA's first piece or unit
+    int64_t u0, u1;
+    const int64_t own_n = cut ? pieces_of(own, q) * H : own_units;
     {
         int64_t base = 0;
         for (int b0 = 0; b0 < p.B; b0 += kThreads) {
             const int b = b0 + tid;
-            const int64_t n = b0 == 0 ? own : b < p.B ? seq_units(seq_of(p, b, false), G, p.window, R) * H : 0;
+            const int64_t n = b0 == 0 ? own_n : b < p.B ? seq_units(seq_of(p, b, false), G, p.window, R) * H : 0;
             int64_t x = n;  // inclusive scan over the CTA
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -206,78 +255,110 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
                 all += red[w];
             }
             x += before;
-            if (n > 0 && u0 >= x - n && u0 < x) {
+            if (n > 0 && at0 >= x - n && at0 < x) {
                 found[0] = b;
                 found[1] = x - n;
             }
             base = all;
-            if (u0 < base) break;
+            if (at0 < base) break;
         }
         __syncthreads();
     }
-    int b = (int)found[0], h, r0 = 0, piece;
-    Seq s = seq_of(p, b, false);
-    int64_t run;  // unit number of the current run's first unit
+    if (found[0] < 0) return;  // past the last piece or unit
+    Run c;
+    c.b = (int)found[0];
+    c.s = seq_of(p, c.b, false);
+    c.r0 = 0;
+    int cut_parts = 0;  // pieces of the run, and the CTA of its first one
+    int64_t cut_first = 0;
     {
-        const int64_t per = seq_units(s, G, p.window, R);
-        int64_t off = u0 - found[1];
-        h = (int)(off / per);
-        off -= h * per;
+        const int64_t per = cut ? pieces_of(c.s, q) : seq_units(c.s, G, p.window, R);
+        int64_t off = at0 - found[1];
+        c.h = fits ? (int)off / (int)per : (int)(off / per);
+        off -= c.h * per;
         int n;
-        while (off >= (n = units_of(s, G, p.window, r0, R))) {
-            off -= n;
-            r0 += R;
+        while (true) {
+            n = units_of(c.s, G, p.window, c.r0, R);
+            const int m = cut ? (n + q - 1) / q : n;
+            if (off < m) break;
+            off -= m;
+            c.r0 += R;
         }
-        piece = (int)off;
-        run = u0 - piece;
+        if (cut) {
+            const int i = (int)off;
+            cut_parts = (n + q - 1) / q;
+            cut_first = blockIdx.x - i;
+            const int base = n / cut_parts, rest = n - base * cut_parts;
+            c.piece = i * base + min(i, rest);
+            u0 = c.piece;
+            u1 = u0 + base + (i < rest);
+        } else {
+            c.piece = (int)off;
+            u0 = at0;
+            u1 = min(u0 + share, total);
+        }
+        c.unit0 = u0 - c.piece;
     }
+    auto measure = [&](Run& r, int64_t u) {
+        range_of(r.s, G, p.window, r.r0, R, r.begin, r.end);
+        r.units = max(1, (r.end - r.begin + kUnit - 1) / kUnit);
+        r.take = (int)min((int64_t)(r.units - r.piece), u1 - u);
+    };
+    measure(c, u0);
 
+    // This warp's ring. Step i of a run's part covers tokens first + i * kUnit ... + kStep, one
+    // record per lane of a pair; the records' addresses are looked up 16 steps at a time.
     uint8_t* ring = smem + warp * (kStages * 2 * REC);
-    float* merge = reinterpret_cast<float*>(smem);
-    uint32_t at = 0, phase = 0;  // ring place and parity of this warp's next step
-    bool alive = true;  // false after a wait that gave up
+    uint32_t taken = 0, given = 0;       // steps taken from the ring, and issued into it
+    const uint8_t* src = nullptr;        // lane 2 i + r: record r of step 16 k + i (null: not there)
+    bool holes = false;                  // a page of the run is not there (every lane knows)
+    bool alive = true;                   // false after a wait that gave up
+    auto first_of = [&](const Run& r) { return r.begin + r.piece * kUnit + warp * kStep; };
+    auto steps_of = [&](const Run& r) {
+        const int first = first_of(r);
+        return first < r.end ? min(r.take, (r.end - first + kUnit - 1) / kUnit) : 0;
+    };
+    auto record = [&](const Run& r, int j) -> const uint8_t* {
+        const int pg = j / p.cache.page_size;
+        const int page = __ldg(p.table + r.b * p.table_stride + pg);
+        if (page < 0 || page >= p.cache.num_pages) return nullptr;
+        return p.cache.pages + (((int64_t)page * H + r.h) * (p.cache.page_size >> 4) + ((j - pg * p.cache.page_size) >> 4)) * REC;
+    };
+    auto issue = [&](const Run& r, int step, int steps) {
+        const int turn = step & 15;
+        if (turn == 0) {
+            const int i = step + (lane >> 1), j = first_of(r) + i * kUnit + 16 * (lane & 1);
+            const bool want = i < steps && j < r.end;
+            src = want ? record(r, j) : nullptr;
+            if (want && !src) report_index(p.err);
+            holes = __any_sync(0xffffffffu, want && !src) || (step > 0 && holes);
+        }
+        if ((lane >> 1) == turn) {
+            const uint32_t to = given % kStages;
+            uint64_t* bar = &full[warp][to];
+            if (src) {
+                mbar_arrive_expect_tx(bar, REC);
+                bulk_load(ring + (2 * to + (lane & 1)) * REC, src, REC, bar);
+            } else {
+                mbar_arrive(bar);
+            }
+        }
+        ++given;
+    };
+    int steps = steps_of(c);
+#pragma unroll
+    for (int i = 0; i < kStages; ++i)
+        if (i < steps) issue(c, i, steps);
+
+    float* merge = reinterpret_cast<float*>(smem + kWarps * kStages * 2 * REC);
     int64_t u = u0;
     while (true) {
         // ---------------------------------------------------------------- one run, or this CTA's part of it
-        int begin, end;
-        range_of(s, G, p.window, r0, R, begin, end);
-        const int units = max(1, (end - begin + kUnit - 1) / kUnit);
-        const int take = (int)min((int64_t)(units - piece), u1 - u);
+        const Seq& s = c.s;
+        const int h = c.h, r0 = c.r0, end = c.end;
         const float gk = p.cache.k_scale ? __ldg(p.cache.k_scale + h) : 1.0f;
         const float gv = p.cache.v_scale ? __ldg(p.cache.v_scale + h) : 1.0f;
-
-        // this warp's steps, and their copies: two records each
-        const int first = begin + piece * kUnit + warp * kStep;
-        const int steps = first < end ? min(take, (end - first + kUnit - 1) / kUnit) : 0;
-        uint32_t bad = 0;           // bits 2 i, 2 i + 1: record 0 or 1 of the step in ring place i is not there
-        uint32_t to = at;           // ring place of the next issue
-        const uint8_t* src = nullptr;  // lane 2 i + r: record r of step 16 k + i (null: not there), 16 steps at a time
-        auto issue = [&](int step) {
-            if ((step & 15) == 0) {
-                const int j = first + (step + (lane >> 1)) * kUnit + 16 * (lane & 1);
-                src = nullptr;
-                if (j < end) {
-                    const int pg = j / p.cache.page_size;
-                    const int page = __ldg(p.table + b * p.table_stride + pg);
-                    if (page >= 0 && page < p.cache.num_pages)
-                        src = p.cache.pages +
-                              (((int64_t)page * H + h) * (p.cache.page_size >> 4) + ((j - pg * p.cache.page_size) >> 4)) * REC;
-                    else if (step + (lane >> 1) < steps)
-                        report_index(p.err);
-                }
-            }
-            const int turn = step & 15;
-            const uint32_t have = (__ballot_sync(0xffffffffu, src != nullptr) >> (2 * turn)) & 3u;
-            bad = (bad & ~(3u << (2 * to))) | ((~have & 3u) << (2 * to));
-            uint64_t* bar = &full[warp][to];
-            if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)__popc(have) * REC);
-            __syncwarp();
-            if ((lane >> 1) == turn && src) bulk_load(ring + to * (2 * REC) + (lane & 1) * REC, src, REC, bar);
-            to = to + 1 == kStages ? 0 : to + 1;
-        };
-#pragma unroll
-        for (int i = 0; i < kStages; ++i)
-            if (i < steps && alive) issue(i);
+        const int first = first_of(c);
 
         // this lane's query elements (row 8 nt + g, d = t D/4 ...) as the second operand, and
         // the scale and limits of its score columns (rows 8 nt + 2t, + 2t + 1)
@@ -287,7 +368,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
         float m[NT][2], l[NT][2];
         float ref[NT][2];    // m - kShift (0 while m is -inf)
         float limit[NT][2];  // the unscaled score that raises m
-        // outputs: with PAIR, o[2 i + e] holds elements e of the d pairs 2 i, 2 i + 1
         float o[KS][NT][4];
         int lim_min = INT_MAX;
 #pragma unroll
@@ -362,67 +442,77 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
         // the last row's window starts last
         const int lo_max = p.window > 0 ? end - p.window : 0;
         const int lo_min = p.window > 0 ? s.len - s.nq + r0 / G + 1 - p.window : 0;
+        // steps [full0, full1): every row sees every token
+        const int full0 = lo_max > first ? (lo_max - first + kUnit - 1) / kUnit : 0;
+        const int full1 = holes || lim_min < first + kStep ? 0 : (min(lim_min, end) - kStep - first) / kUnit + 1;
 
-        for (int step = 0; step < steps && alive; ++step) {
-            if (!mbar_wait_err(&full[warp][at], phase, p.err)) alive = false;
-            if (!__all_sync(0xffffffffu, alive)) {
-                // give the copies behind it their (bounded) time, then leave
-                alive = false;
-                for (int i = 1; i < min(steps - step, kStages); ++i) {
-                    const uint32_t x = at + i;
-                    mbar_wait_err(&full[warp][x % kStages], phase ^ (x >= kStages), p.err);
-                }
-                break;
-            }
+        for (int step = 0; step < steps; ++step) {
+            const uint32_t at = taken % kStages;
+            // the warp decides together; after a wait that gave up (reported) nothing is issued
+            // or waited for any more
+            const uint32_t parity = (taken / kStages) & 1u;
+            if (__any_sync(0xffffffffu, !mbar_try_wait(&full[warp][at], parity)) && alive)
+                alive = __all_sync(0xffffffffu, mbar_wait_err(&full[warp][at], parity, p.err));
+            ++taken;
             const uint8_t* buf = ring + at * (2 * REC);
             const int j0 = first + step * kUnit;
-            const uint32_t lost = (bad >> (2 * at)) & 3u;
-            // every row sees every token of the step
-            const bool whole = j0 + kStep <= lim_min && j0 >= lo_max && lost == 0;
+            const bool whole = step >= full0 && step < full1 && !holes;
+            // records that are not there: looked up again, since nothing but a bad page comes here
+            uint32_t lost = 0;
+            if (holes)
+                for (int r = 0; r < 2; ++r)
+                    if (j0 + 16 * r < end && !record(c, j0 + 16 * r)) lost |= 1u << r;
 
-            // ---- scores
+            // ---- scores: the two records side by side, as independent chains of products
             float z[2][NT][4];
+            uint32_t ka[2][KS / 4], kb[2][KS / 4], ka2[2][KS / 4], kb2[2][KS / 4];  // tokens g and g + 8: low and high half of the lane's codes
+            __half2 sa[2][2], sb[2][2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const uint8_t* rec = buf + r * REC;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) z[r][nt][c] = 0.0f;
-                uint32_t ka[KS / 2], kb[KS / 2], s0, s1;  // tokens g and g + 8
-                uint32_t sa[2], sb[2];
+                uint32_t s0, s1;
                 if constexpr (D == 128) {
                     const uint4 x = *reinterpret_cast<const uint4*>(rec + g * 64 + t * 16);
                     const uint4 y = *reinterpret_cast<const uint4*>(rec + 512 + g * 64 + t * 16);
-                    ka[0] = x.x, ka[1] = x.y, ka[2] = x.z, ka[3] = x.w;
-                    kb[0] = y.x, kb[1] = y.y, kb[2] = y.z, kb[3] = y.w;
+                    ka[r][0] = x.x, ka[r][1] = x.y, ka2[r][0] = x.z, ka2[r][1] = x.w;
+                    kb[r][0] = y.x, kb[r][1] = y.y, kb2[r][0] = y.z, kb2[r][1] = y.w;
                     e4m3x4_half(*reinterpret_cast<const uint32_t*>(rec + 16 * D + lane * 4), s0, s1);
-                    sa[0] = low2(s0), sa[1] = high2(s0), sb[0] = low2(s1), sb[1] = high2(s1);
+                    sa[r][0] = low2(s0), sa[r][1] = high2(s0), sb[r][0] = low2(s1), sb[r][1] = high2(s1);
                 } else {
                     const uint2 x = *reinterpret_cast<const uint2*>(rec + g * 32 + t * 8);
                     const uint2 y = *reinterpret_cast<const uint2*>(rec + 256 + g * 32 + t * 8);
-                    ka[0] = x.x, ka[1] = x.y;
-                    kb[0] = y.x, kb[1] = y.y;
+                    ka[r][0] = x.x, ka2[r][0] = x.y;
+                    kb[r][0] = y.x, kb2[r][0] = y.y;
                     // a lane pair's two scales each lie in one word
-                    const uint32_t w = *reinterpret_cast<const uint32_t*>(rec + 16 * D + (lane >> 1) * 4);
-                    e4m3x4_half(w, s0, s1);
+                    e4m3x4_half(*reinterpret_cast<const uint32_t*>(rec + 16 * D + (lane >> 1) * 4), s0, s1);
                     const uint32_t mine2 = (lane & 1) ? s1 : s0;
-                    sa[0] = sa[1] = low2(mine2), sb[0] = sb[1] = high2(mine2);
+                    sa[r][0] = sa[r][1] = low2(mine2), sb[r][0] = sb[r][1] = high2(mine2);
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < KS / 2; ++w) {
+                constexpr int HALF = KS / 4;
+                uint32_t x[2][4], y[2][4];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    e2m1x8_half(w < HALF ? ka[r][w] : ka2[r][w - HALF], x[r]);
+                    e2m1x8_half(w < HALF ? kb[r][w] : kb2[r][w - HALF], y[r]);
                 }
 #pragma unroll
-                for (int w = 0; w < KS / 2; ++w) {
-                    uint32_t x[4], y[4];
-                    e2m1x8_half(ka[w], x);
-                    e2m1x8_half(kb[w], y);
-                    const uint32_t fa = sa[2 * w / (KS / 2)], fb = sb[2 * w / (KS / 2)];
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t a[4] = {mul_h2(x[2 * i], fa), mul_h2(y[2 * i], fb), mul_h2(x[2 * i + 1], fa),
-                                               mul_h2(y[2 * i + 1], fb)};
+                    for (int r = 0; r < 2; ++r) {
+                        const __half2 fa = sa[r][w / HALF], fb = sb[r][w / HALF];
+                        const uint32_t a[4] = {mul_h2(x[r][2 * i], fa), mul_h2(y[r][2 * i], fb), mul_h2(x[r][2 * i + 1], fa),
+                                               mul_h2(y[r][2 * i + 1], fb)};
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma_f16(z[r][nt], a, qf[nt][2 * w + i][0], qf[nt][2 * w + i][1]);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (w == 0 && i == 0)
+                                mma_f16_first(z[r][nt], a, qf[nt][0][0], qf[nt][0][1]);
+                            else
+                                mma_f16(z[r][nt], a, qf[nt][2 * w + i][0], qf[nt][2 * w + i][1]);
+                        }
                     }
-                }
             }
             if (!whole) {
 #pragma unroll
@@ -501,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
                 }
                 uint32_t sab, scd;
                 e4m3x4_half(sc, sab, scd);
-                const uint32_t f[4] = {low2(sab), high2(sab), low2(scd), high2(scd)};  // tokens 2t, 2t+1, 2t+8, 2t+9
+                const __half2 f[4] = {low2(sab), high2(sab), low2(scd), high2(scd)};  // tokens 2t, 2t+1, 2t+8, 2t+9
                 uint32_t v[4][KS / 4];                                                // their codes of this lane's d
                 if constexpr (D == 128) {
                     const uint8_t* base = rec + 8 * D + g * 128 + t * 16;
@@ -525,23 +615,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
 #pragma unroll
                         for (int e = 0; e < 4; ++e) x[i][e] = mul_h2(x[i][e], f[i]);
                     }
-                    if constexpr (PAIR) {
-                        // the product's k pair is the two d of a byte, its row a byte: against (p, 0)
-                        // it sums the even d, against (0, p) the odd ones, eight tokens a product
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {  // tokens 0..7, 8..15
-                                const uint32_t a[4] = {x[2 * e][2 * i], x[2 * e][2 * i + 1], x[2 * e + 1][2 * i],
-                                                       x[2 * e + 1][2 * i + 1]};
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) {
-                                    const uint32_t pr = pb[r][nt][e];
-                                    mma_f16(o[2 * (2 * w + i)][nt], a, pr & 0xFFFFu, pr >> 16);
-                                    mma_f16(o[2 * (2 * w + i) + 1][nt], a, pr << 16, pr & 0xFFFF0000u);
-                                }
-                            }
-                    } else
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const uint32_t a[4] = {__byte_perm(x[0][e], x[1][e], 0x5410), __byte_perm(x[0][e], x[1][e], 0x7632),
@@ -552,12 +625,34 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
                 }
             }
             __syncwarp();
-            if (step + kStages < steps) issue(step + kStages);
-            if (++at == kStages) at = 0, phase ^= 1u;
+            if (step + kStages < steps && alive) issue(c, step + kStages, steps);
+        }
+
+        // the next run's first copies fly while this one is joined
+        u += c.take;
+        Run nx = c;
+        int nsteps = 0;
+        if (u < u1) {
+            nx.unit0 += nx.units;
+            nx.piece = 0;
+            nx.r0 += R;
+            if (nx.r0 >= nx.s.nq * G) {
+                nx.r0 = 0;
+                if (++nx.h == H) {
+                    nx.h = 0;
+                    do nx.s = seq_of(p, ++nx.b, false);
+                    while (nx.s.nq == 0);
+                }
+            }
+            measure(nx, u);
+            nsteps = steps_of(nx);
+#pragma unroll
+            for (int i = 0; i < kStages; ++i)
+                if (i < nsteps && alive) issue(nx, i, nsteps);
         }
 
         // ---------------------------------------------------------------- join the warps
-        // Without PAIR, o[j][.][c] is d = g D/8 + 2 j + (c >> 1). A merged row lies as [j][g][2] (d = g D/8 + 2 j + .), RS floats.
+        // o[j][.][c] is d = g D/8 + 2 j + (c >> 1). A merged row lies as [j][g][2], RS floats.
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -572,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
                     sm_m[warp][8 * nt + 2 * t + c] = m[nt][c];
                     sm_l[warp][8 * nt + 2 * t + c] = l[nt][c];
                 }
-        __syncthreads();  // every ring is idle: its memory takes the merge
+        __syncthreads();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -585,19 +680,18 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
                 float2* dst = reinterpret_cast<float2*>(merge + (warp * R + row) * RS) + g;
 #pragma unroll
                 for (int j = 0; j < KS; ++j)
-                    dst[8 * j] = PAIR ? make_float2(o[j & ~1][nt][c + 2 * (j & 1)] * f, o[j | 1][nt][c + 2 * (j & 1)] * f)
-                                      : make_float2(o[j][nt][c] * f, o[j][nt][c + 2] * f);
+                    dst[8 * j] = make_float2(o[j][nt][c] * f, o[j][nt][c + 2] * f);
             }
         __syncthreads();
         const int rows = min(R, s.nq * G - r0);
-        const int64_t w_first = run / share, w_last = (run + units - 1) / share;
-        const int parts = (int)(w_last - w_first + 1);
+        const int64_t w_first = cut ? cut_first : c.unit0 / share;
+        const int parts = cut ? cut_parts : (int)((c.unit0 + c.units - 1) / share - w_first + 1);
         constexpr int PAIRS = D / 2, RPP = kThreads / PAIRS;  // float2s of a row, rows per pass
         const int pi = tid % PAIRS;                           // output elements 2 pi, 2 pi + 1
         const int pg = pi / KS, pj = pi % KS;
         if (parts > 1) {
             // slot 0 of a CTA: a run that an earlier CTA began; slot 1: one that it begins itself
-            const int64_t slot = 2 * (int64_t)blockIdx.x + (run < u0 ? 0 : 1);
+            const int64_t slot = 2 * (int64_t)blockIdx.x + (c.unit0 < u0 ? 0 : 1);
             float* dst = p.partial + slot * slot_floats(NT, D);
             for (int row = tid / PAIRS; row < rows; row += RPP) {
                 float2 a = make_float2(0.0f, 0.0f);
@@ -619,15 +713,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
                     dst[R * D + R + row] = sum;
                 }
             }
-            __threadfence();
             __syncthreads();
             if (tid == 0) {
-                const int old = atomicAdd(p.counters + w_first, 1);
+                // release what the CTA wrote, acquire what the other parts' CTAs released
+                int old;
+                asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(p.counters + w_first) : "memory");
                 last_part = old == parts - 1;
                 if (last_part) p.counters[w_first] = 0;
             }
             __syncthreads();
-            if (last_part) __threadfence();
         }
         if (parts == 1) {
             for (int row = tid / PAIRS; row < rows; row += RPP) {
@@ -656,16 +750,21 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
             const float* part0 = p.partial + (2 * w_first + 1) * SLOT;
             const float* parts1 = p.partial + 2 * w_first * SLOT;  // part i > 0 at + 2 i SLOT
             float* fac = merge;                                    // [parts][R]: the merge's rows are not needed any more
+            // the first 32 parts' maxima and sums, read together
+            auto stat = [&](int i, int row) { return (i ? parts1 + (int64_t)2 * i * SLOT : part0) + R * D + row; };
             for (int row = warp; row < rows; row += kWarps) {
-                float top = -INFINITY, sum = 0.0f;
-                for (int i = lane; i < parts; i += 32)
-                    top = fmaxf(top, __ldcg((i ? parts1 + (int64_t)2 * i * SLOT : part0) + R * D + row));
+                const float m0 = lane < parts ? __ldcg(stat(lane, row)) : -INFINITY;
+                const float l0 = lane < parts ? __ldcg(stat(lane, row) + R) : 0.0f;
+                float top = m0;
+                for (int i = lane + 32; i < parts; i += 32) top = fmaxf(top, __ldcg(stat(i, row)));
                 top = warp_max(top);
-                for (int i = lane; i < parts; i += 32) {
-                    const float* src = (i ? parts1 + (int64_t)2 * i * SLOT : part0) + R * D + row;
-                    const float mw = __ldcg(src), f = mw == -INFINITY ? 0.0f : ex2(mw - top);
+                const float f0 = m0 == -INFINITY ? 0.0f : ex2(m0 - top);
+                float sum = l0 * f0;
+                if (lane < parts) fac[lane * R + row] = f0;
+                for (int i = lane + 32; i < parts; i += 32) {
+                    const float mw = __ldcg(stat(i, row)), f = mw == -INFINITY ? 0.0f : ex2(mw - top);
                     fac[i * R + row] = f;
-                    sum = __fmaf_rn(__ldcg(src + R), f, sum);
+                    sum = __fmaf_rn(__ldcg(stat(i, row) + R), f, sum);
                 }
 #pragma unroll
                 for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
@@ -675,26 +774,28 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
                 }
             }
             __syncthreads();
+#pragma unroll 2
             for (int i = tid; i < rows * QUADS; i += kThreads) {
                 const int row = i / QUADS, d = 4 * (i - row * QUADS);
                 float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                auto add = [&](const float4& v, float f) {
-                    a.x = __fmaf_rn(v.x, f, a.x);
-                    a.y = __fmaf_rn(v.y, f, a.y);
-                    a.z = __fmaf_rn(v.z, f, a.z);
-                    a.w = __fmaf_rn(v.w, f, a.w);
-                };
-                add(__ldcg(reinterpret_cast<const float4*>(part0 + row * D + d)), fac[row]);
-                const float* src = parts1 + row * D + d;
-                int w = 1;
-                for (; w + 8 <= parts; w += 8) {
+                for (int w = 0; w < parts; w += 8) {
                     float4 v[8];
+                    float f[8];
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) v[x] = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)2 * (w + x) * SLOT));
+                    for (int x = 0; x < 8; ++x) {
+                        const bool on = w + x < parts;
+                        const float* from = (w + x ? parts1 + (int64_t)2 * (w + x) * SLOT : part0) + row * D + d;
+                        v[x] = on ? __ldcg(reinterpret_cast<const float4*>(from)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        f[x] = on ? fac[(w + x) * R + row] : 0.0f;
+                    }
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) add(v[x], fac[(w + x) * R + row]);
+                    for (int x = 0; x < 8; ++x) {
+                        a.x = __fmaf_rn(v[x].x, f[x], a.x);
+                        a.y = __fmaf_rn(v[x].y, f[x], a.y);
+                        a.z = __fmaf_rn(v[x].z, f[x], a.z);
+                        a.w = __fmaf_rn(v[x].w, f[x], a.w);
+                    }
                 }
-                for (; w < parts; ++w) add(__ldcg(reinterpret_cast<const float4*>(src + (int64_t)2 * w * SLOT)), fac[w * R + row]);
                 const int qi = (r0 + row) / G, hq = h * G + r0 + row - qi * G;
                 const int64_t tok = s.row0 + qi;
                 const float sum = sm_l[0][row], inv = sum > 0.0f ? gv / sum : 0.0f;
@@ -704,38 +805,33 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
             }
         }
         // ---------------------------------------------------------------- the next run
-        u += take;
         if (u >= u1) break;
-        fence_proxy_async_smem();  // the merge's writes come before the ring's next copies
-        __syncthreads();
-        run += units;
-        piece = 0;
-        r0 += R;
-        if (r0 >= s.nq * G) {
-            r0 = 0;
-            if (++h == H) {
-                h = 0;
-                do s = seq_of(p, ++b, false);
-                while (s.nq == 0);
-            }
-        }
+        c = nx;
+        steps = nsteps;
+        __syncthreads();  // the merge's memory is free again
     }
+    // a warp that gave up leaves its last copies their (bounded) time
+    if (!alive)
+        for (uint32_t i = 1; i <= min(given, (uint32_t)kStages); ++i)
+            mbar_wait_err(&full[warp][(given - i) % kStages], ((given - i) / kStages) & 1u, p.err);
 }
 
+// Rings, then the memory of a merge: the warps' rows, or a run's factors (at most one part a CTA).
 template <int D, int NT>
-constexpr size_t smem_bytes() {
-    const size_t ring = (size_t)kWarps * kStages * 2 * 18 * D, merge = (size_t)kWarps * 8 * NT * (D + 4) * 4;
-    return ring > merge ? ring : merge;
+size_t smem_bytes(int grid) {
+    const size_t rows = (size_t)kWarps * 8 * NT * (D + 4) * 4, factors = (size_t)grid * 8 * NT * 4;
+    return (size_t)kWarps * kStages * 2 * 18 * D + (rows > factors ? rows : factors);
 }
 
 template <int D, int NT, bool F16>
 cudaError_t attn_of(const AttnParams& p, int grid, cudaStream_t s) {
     static std::atomic<bool> done[64];
-    const cudaError_t e = once_per_device(done, [] {
-        return cudaFuncSetAttribute(k_attn<D, NT, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D, NT>());
+    const size_t smem = smem_bytes<D, NT>(grid);
+    const cudaError_t e = once_per_device(done, [smem] {
+        return cudaFuncSetAttribute(k_attn<D, NT, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     });
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_attn<D, NT, F16>, dim3(grid), dim3(kThreads), smem_bytes<D, NT>(), s, 1, p);
+    return launch_pdl(k_attn<D, NT, F16>, dim3(grid), dim3(kThreads), smem, s, 1, p);
 }
 
 int row_tiles(int q_heads, int kv_heads, int max_q) {
