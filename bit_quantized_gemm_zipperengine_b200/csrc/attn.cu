@@ -117,24 +117,24 @@ __device__ __forceinline__ Seq seq_of(const AttnParams& p, int b, bool report) {
 }
 // The tokens that rows [r0, r0 + rows) of a sequence's nq * G rows can see: [begin, end), begin
 // rounded down to a step.
-__device__ __forceinline__ void range_of(const Seq& s, int G, int window, int r0, int rows, int& begin, int& end) {
-    const int last = min(r0 + rows, s.nq * G) - 1;
-    end = max(0, s.len - s.nq + last / G + 1);
+__device__ __forceinline__ void range_of(const Seq& s, const FastDiv& G, int window, int r0, int rows, int& begin, int& end) {
+    const int last = min(r0 + rows, s.nq * G.d) - 1;
+    end = max(0, s.len - s.nq + (int)G.div(last) + 1);
     begin = 0;
     if (window > 0) {
-        const int64_t lo = (int64_t)s.len - s.nq + r0 / G - window + 1;
+        const int64_t lo = (int64_t)s.len - s.nq + (int)G.div(r0) - window + 1;
         begin = lo > 0 ? (int)lo / kStep * kStep : 0;
     }
 }
-__device__ __forceinline__ int units_of(const Seq& s, int G, int window, int r0, int rows) {
+__device__ __forceinline__ int units_of(const Seq& s, const FastDiv& G, int window, int r0, int rows) {
     int begin, end;
     range_of(s, G, window, r0, rows, begin, end);
     return max(1, (end - begin + kUnit - 1) / kUnit);  // one for rows that see nothing: they are written too
 }
 // Units of one cache head of a sequence.
-__device__ __forceinline__ int64_t seq_units(const Seq& s, int G, int window, int rows) {
+__device__ __forceinline__ int64_t seq_units(const Seq& s, const FastDiv& G, int window, int rows) {
     int64_t n = 0;
-    for (int r0 = 0; r0 < s.nq * G; r0 += rows) n += units_of(s, G, window, r0, rows);
+    for (int r0 = 0; r0 < s.nq * G.d; r0 += rows) n += units_of(s, G, window, r0, rows);
     return n;
 }
 
@@ -172,27 +172,28 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
     __shared__ uint64_t full[kWarps][kStages];
     __shared__ float sm_m[kWarps][R], sm_l[kWarps][R];
     __shared__ int64_t red[kWarps], red2[kWarps];
-    __shared__ int64_t found[4];
+    __shared__ int64_t found[2];
+    __shared__ int counts[kWarps];
     __shared__ int last_part;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int H = p.cache.heads, G = p.q.heads / H;
+    const int H = p.cache.heads;
+    const FastDiv& G = p.by_group;
     if (tid < kWarps * kStages) mbar_init(&full[0][0] + tid, 2);  // the two records' lanes
     mbar_fence_init();
     griddep_wait();
     griddep_launch();
 
     // The CTA's work. CTA w takes the w-th equal share of all units, in order; or, with fewer
-    // runs than CTAs, every run is cut into equal pieces of at most q units, one CTA each, q the
-    // least for which the CTAs suffice. Then no CTA joins two runs, which costs it about as
+    // runs than CTAs, every run is cut into equal pieces of at most q units, one CTA each. Then no CTA joins two runs, which costs it about as
     // much as kJoin units (16 sequences of up to 8192 tokens: 33.2 us by shares, 31.8 by pieces;
     // 4 of 131072, where pieces waste 5 of 74 units: 126.6 and 132.7).
     const Seq own = tid < p.B ? seq_of(p, tid, blockIdx.x == 0) : Seq{0, 0, 0};
     const int64_t own_units = seq_units(own, G, p.window, R) * H;
-    int64_t mine = own_units, rmine = (int64_t)((own.nq * G + R - 1) / R) * H;
+    int64_t mine = own_units, rmine = (int64_t)((own.nq * G.d + R - 1) / R) * H;
     for (int b = tid + kThreads; b < p.B; b += kThreads) {
         const Seq s = seq_of(p, b, blockIdx.x == 0);
         mine += seq_units(s, G, p.window, R) * H;
-        rmine += (int64_t)((s.nq * G + R - 1) / R) * H;
+        rmine += (int64_t)((s.nq * G.d + R - 1) / R) * H;
     }
     mine = warp_sum(mine);
     rmine = warp_sum(rmine);
@@ -211,24 +212,23 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
     if (total == 0) return;
     const int grid = (int)gridDim.x;
     const bool fits = total < (1 << 30);  // 32-bit divisions
-    const int64_t share = fits ? ((int)total + grid - 1) / grid : (total + grid - 1) / grid;
+    const int64_t share = fits ? (int)p.by_grid.div((uint32_t)total + grid - 1) : (total + grid - 1) / grid;
     auto pieces_of = [&](const Seq& s, int q) {  // of one cache head
         int n = 0;
-        for (int r0 = 0; r0 < s.nq * G; r0 += R) n += (units_of(s, G, p.window, r0, R) + q - 1) / q;
+        for (int r0 = 0; r0 < s.nq * G.d; r0 += R) n += (units_of(s, G, p.window, r0, R) + q - 1) / q;
         return n;
     };
     bool cut = false;
-    int q = (int)share;
+    int q = 1;
     if (fits && p.B <= kThreads && runs < grid) {
-        for (; q <= (int)share + kJoin && !cut; q += !cut) {
+        // a run's last piece is half empty on average
+        const int room = grid - (int)runs / 2;
+        q = ((int)total + room - 1) / room;
+        if (q <= (int)share + kJoin) {
             const int n = __reduce_add_sync(0xffffffffu, pieces_of(own, q) * H);
+            if (lane == 0) counts[warp] = n;
             __syncthreads();
-            if (lane == 0) red[warp] = n;
-            __syncthreads();
-            int sum = 0;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) sum += (int)red[w];
-            cut = sum <= grid;
+            cut = counts[0] + counts[1] + counts[2] + counts[3] <= grid;
         }
     }
     const int64_t at0 = cut ? blockIdx.x : share * blockIdx.x;  // the CTA's first piece or unit
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
         return first < r.end ? min(r.take, (r.end - first + kUnit - 1) / kUnit) : 0;
     };
     auto record = [&](const Run& r, int j) -> const uint8_t* {
-        const int pg = j / p.cache.page_size;
+        const int pg = (int)p.by_page.div(j);
         const int page = __ldg(p.table + r.b * p.table_stride + pg);
         if (page < 0 || page >= p.cache.num_pages) return nullptr;
         return p.cache.pages + (((int64_t)page * H + r.h) * (p.cache.page_size >> 4) + ((j - pg * p.cache.page_size) >> 4)) * REC;
@@ -372,14 +372,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
         int lim_min = INT_MAX;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int row = r0 + 8 * nt + g, rows = s.nq * G;
+            const int row = r0 + 8 * nt + g, rows = s.nq * G.d;
             float inv = 0.0f;
 #pragma unroll
             for (int j = 0; j < KS; ++j) qf[nt][j][0] = qf[nt][j][1] = 0u;
             if (row < rows) {
-                const int qi = row / G;
+                const int qi = (int)G.div(row);
                 const uint4* src = reinterpret_cast<const uint4*>(p.q.p + (int64_t)(s.row0 + qi) * p.q.st +
-                                                                  (int64_t)(h * G + row - qi * G) * p.q.sh + t * (D / 4));
+                                                                  (int64_t)(h * G.d + row - qi * G.d) * p.q.sh + t * (D / 4));
 #pragma unroll
                 for (int i = 0; i < KS / 2; ++i) {
                     const uint4 v = __ldg(src + i);
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
             for (int c = 0; c < 2; ++c) {
                 qs[nt][c] = __shfl_sync(0xffffffffu, z, 4 * (2 * t + c));
                 const int r = r0 + 8 * nt + 2 * t + c;
-                lim[nt][c] = r < rows ? s.len - s.nq + r / G + 1 : INT_MAX;
+                lim[nt][c] = r < rows ? s.len - s.nq + (int)G.div(r) + 1 : INT_MAX;
                 lim_min = min(lim_min, lim[nt][c]);
                 m[nt][c] = -INFINITY;
                 ref[nt][c] = 0.0f;
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
         lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, 2));
         // the last row's window starts last
         const int lo_max = p.window > 0 ? end - p.window : 0;
-        const int lo_min = p.window > 0 ? s.len - s.nq + r0 / G + 1 - p.window : 0;
+        const int lo_min = p.window > 0 ? s.len - s.nq + (int)G.div(r0) + 1 - p.window : 0;
         // steps [full0, full1): every row sees every token
         const int full0 = lo_max > first ? (lo_max - first + kUnit - 1) / kUnit : 0;
         const int full1 = holes || lim_min < first + kStep ? 0 : (min(lim_min, end) - kStep - first) / kUnit + 1;
@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
             nx.unit0 += nx.units;
             nx.piece = 0;
             nx.r0 += R;
-            if (nx.r0 >= nx.s.nq * G) {
+            if (nx.r0 >= nx.s.nq * G.d) {
                 nx.r0 = 0;
                 if (++nx.h == H) {
                     nx.h = 0;
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
                     dst[8 * j] = make_float2(o[j][nt][c] * f, o[j][nt][c + 2] * f);
             }
         __syncthreads();
-        const int rows = min(R, s.nq * G - r0);
+        const int rows = min(R, s.nq * G.d - r0);
         const int64_t w_first = cut ? cut_first : c.unit0 / share;
         const int parts = cut ? cut_parts : (int)((c.unit0 + c.units - 1) / share - w_first + 1);
         constexpr int PAIRS = D / 2, RPP = kThreads / PAIRS;  // float2s of a row, rows per pass
@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
                     a.y += v.y;
                     sum += sm_m[w][row] == -INFINITY ? 0.0f : sm_l[w][row] * ex2(sm_m[w][row] - top);
                 }
-                const int qi = (r0 + row) / G, hq = h * G + r0 + row - qi * G;
+                const int qi = (int)G.div(r0 + row), hq = h * G.d + r0 + row - qi * G.d;
                 const int64_t tok = s.row0 + qi;
                 const float inv = sum > 0.0f ? gv / sum : 0.0f;
                 *reinterpret_cast<uint32_t*>(p.o.p + tok * p.o.st + hq * p.o.sh + 2 * pi) = narrow2<F16>(a.x * inv, a.y * inv);
@@ -796,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
                         a.w = __fmaf_rn(v[x].w, f[x], a.w);
                     }
                 }
-                const int qi = (r0 + row) / G, hq = h * G + r0 + row - qi * G;
+                const int qi = (int)G.div(r0 + row), hq = h * G.d + r0 + row - qi * G.d;
                 const int64_t tok = s.row0 + qi;
                 const float sum = sm_l[0][row], inv = sum > 0.0f ? gv / sum : 0.0f;
                 *reinterpret_cast<uint2*>(p.o.p + tok * p.o.st + hq * p.o.sh + d) =
@@ -850,8 +850,11 @@ size_t attn_workspace(int q_heads, int kv_heads, int D, int max_q, size_t* count
 
 cudaError_t launch_attn(const AttnParams& p0, int D, int max_q, bool f16, cudaStream_t s) {
     AttnParams p = p0;
+    p.by_group = FastDiv(p.q.heads / p.cache.heads);
+    p.by_page = FastDiv(p.cache.page_size);
     p.scale *= 1.4426950408889634f;  // scores in powers of two
     const int nt = row_tiles(p.q.heads, p.cache.heads, max_q), grid = grid_of(nt);
+    p.by_grid = FastDiv(grid);
     if (D == 64) {
         if (nt == 1) return f16 ? attn_of<64, 1, true>(p, grid, s) : attn_of<64, 1, false>(p, grid, s);
         return f16 ? attn_of<64, 2, true>(p, grid, s) : attn_of<64, 2, false>(p, grid, s);

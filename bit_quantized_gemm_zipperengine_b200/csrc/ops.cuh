@@ -90,6 +90,20 @@ struct GemvParams {
     int w_ready;  // the weight was complete before this kernel could start
 };
 
+// Division of n < 2^31 by d >= 1, d known on the host: a multiply and a shift (Granlund and
+// Montgomery's round-up method).
+struct FastDiv {
+    int d;
+    uint32_t mul;
+    int shift;
+    FastDiv() = default;
+    explicit FastDiv(int divisor) : d(divisor), shift(0) {
+        while ((int64_t(1) << shift) < d) ++shift;
+        mul = (uint32_t)(((uint64_t(1) << 32) * ((uint64_t(1) << shift) - (uint64_t)d)) / (uint64_t)d + 1);
+    }
+    __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
 struct AttnParams {
     HeadsView q, o;
     float* lse;  // [T][heads] or null
@@ -105,6 +119,7 @@ struct AttnParams {
     float* partial;
     int* counters;
     int* err;
+    FastDiv by_group, by_page, by_grid;  // query heads of a cache head, tokens of a page, CTAs
 };
 
 // api.cu: a launch's status, counted in mq_launch_count; the current device's error word
