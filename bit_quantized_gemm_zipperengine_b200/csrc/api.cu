@@ -142,6 +142,10 @@ namespace mq {
 // For the operators of ops.cu.
 mq_status count_launches(cudaError_t e, int kernels) { return launched(e, kernels); }
 int* device_error_word() { return err_word(); }
+bool tensor_map_bytes(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_bytes,
+                      uint32_t box_rows) {
+    return make_tmap_bytes(map, base, row_bytes, rows, box_bytes, box_rows);
+}
 
 }  // namespace mq
 

@@ -1,7 +1,26 @@
 // Products of a few tokens of 16-bit activations with the packed NVFP4 weight:
 //   Y[m,n] = rn(g_w * sum_k x[m,k] (wh[n,k] + [block selected] rh[n,k])),  wh = val * dec(sf).
-// The floor is the weight's bytes (9/16 a weight, 2304 a residual block), read once.
-// One warp a row; a lane takes 32 codes (16 bytes, two scale groups) at a time.
+//
+// What bounds it: the weight's bytes (9/16 a weight, 2304 a residual block), read once.
+//
+// The work of 64 weight rows is a list of steps: 256 columns of the base each, then four
+// residual blocks each (a block row's blocks lie one behind the other). In both a lane of
+// a warp takes 64 adjacent columns of its rows, at a column of its own, which a product's
+// free order of k allows; so a residual step is as dense as a base step. A step's codes
+// (8 KB, one TMA box, 128-byte swizzle; or four packed blocks, one bulk copy) and scales
+// (2 KB, one bulk copy) go to the warp's own ring in shared memory.
+//
+// The weights are the 16-row operand of fp16 tensor-core products (val * dec(sf) is exact
+// in fp16), eight tokens the other one. bf16 activations are scaled by a power of two per
+// token and step to fit fp16 (what falls below is under 2^-39 of the step's largest), and the
+// step's fp32 sums scaled back.
+//
+// The steps of a row tile are dealt to the warps of a cluster of S CTAs, S so that the CTAs
+// about fill the GPU; the warps' sums are added in their order through shared memory, then
+// the CTAs' through the cluster's.
+#include <algorithm>
+
+#include "half_mma.cuh"
 #include "ops.cuh"
 
 namespace mq {
@@ -9,76 +28,272 @@ namespace mq {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kStages = 2;
+constexpr int kRows = 64;              // weight rows of a tile (a block row)
+constexpr int kCols = 256;             // base columns of a step
+constexpr int kCodes = kRows * kCols / 2;
+constexpr int kStage = kCodes + 2048;  // codes, then four 512-byte scale chunks
+constexpr int kCtasPerSm = 2;
+constexpr int kPitch = kRows + 4;      // floats of a token's row in the sums
 
-// acc[m] += sum over 32 elements at column k0: 16 bytes of codes and their two scales.
-template <int MT, bool F16>
-__device__ __forceinline__ void fma32(const GemvParams& p, const uint4& w, float s0, float s1, int k0, int m0,
-                                      float (&acc)[MT]) {
-    const uint32_t c[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float v[8];
-        e2m1x8_values(c[j], v);
-        const float s = j < 2 ? s0 : s1;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= s;  // exact: six significant bits
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            if (m0 + m >= p.M) break;
-            const uint4 xv = __ldg(reinterpret_cast<const uint4*>(p.X + (m0 + m) * p.ldx + k0 + 8 * j));
-            const uint32_t x[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = widen2<F16>(x[i]);
-                acc[m] = __fmaf_rn(f.x, v[2 * i], acc[m]);
-                acc[m] = __fmaf_rn(f.y, v[2 * i + 1], acc[m]);
+template <int NT>
+constexpr size_t smem_bytes() { return (size_t)kWarps * (kStages * kStage + NT * 4096 + kStages * 8); }
+
+template <int NT, bool F16>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) k_gemv(const __grid_constant__ CUtensorMap tw, const GemvParams p) {
+    // The swizzle's pattern repeats every 1024 bytes. Without static shared memory the array
+    // starts on such a boundary (checked below), and two CTAs fit an SM.
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint64_t(*full)[kStages] = reinterpret_cast<uint64_t(*)[kStages]>(smem + kWarps * (kStages * kStage + NT * 4096));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int tile = blockIdx.y, S = gridDim.x, rank = blockIdx.x, KC = p.K / 64;
+    if (tid < kWarps * kStages) mbar_init(&full[0][0] + tid, 1);
+    mbar_fence_init();
+    if (tid == 0) tma_prefetch_desc(&tw);
+    __syncthreads();
+    if (!p.w_ready) {
+        griddep_wait();
+        griddep_launch();
+    }
+    if (smem_u32(smem) & 1023u) {
+        if (tid == 0) report_index(p.err);
+        return;
+    }
+    const int res0 = p.blk_codes ? __ldg(p.tile_ptr + tile) : 0, res1 = p.blk_codes ? __ldg(p.tile_ptr + tile + 1) : 0;
+    const int nbase = p.base ? (KC + 3) / 4 : 0, total = nbase + (res1 - res0 + 3) / 4;
+    const int step0 = rank * kWarps + warp, stride = S * kWarps;
+    const int steps = step0 < total ? (total - step0 + stride - 1) / stride : 0;
+    uint8_t* ring = smem + warp * (kStages * kStage);
+    uint8_t* frag = smem + kWarps * kStages * kStage + warp * (NT * 4096);  // this warp's activations as fp16 operands
+
+    auto issue = [&](int i) {
+        if (lane == 0) {
+            const int step = step0 + i * stride;
+            uint8_t* dst = ring + (i % kStages) * kStage;
+            uint64_t* bar = &full[warp][i % kStages];
+            if (step < nbase) {
+                const uint32_t sf = (uint32_t)min(4, KC - 4 * step) * 512;
+                mbar_arrive_expect_tx(bar, kCodes + sf);
+                tma_load_2d(dst, &tw, bar, step * (kCols / 2), tile * kRows);
+                bulk_load(dst + kCodes, p.sf + ((int64_t)(tile >> 1) * KC + 4 * step) * 512, sf, bar);
+            } else {
+                const int e = res0 + 4 * (step - nbase);
+                const uint32_t n = (uint32_t)min(4, res1 - e);
+                mbar_arrive_expect_tx(bar, n * 2560);
+                bulk_load(dst, p.blk_codes + (int64_t)e * 2048, n * 2048, bar);
+                bulk_load(dst + kCodes, p.blk_sf + (int64_t)e * 512, n * 512, bar);
             }
         }
+    };
+    // Column chunk (64 columns) of this lane in a step, -1 past the end.
+    auto chunk_of = [&](int i) {
+        const int step = step0 + i * stride;
+        if (step < nbase) return 4 * step + t < KC ? 4 * step + t : -1;
+        const int e = res0 + 4 * (step - nbase) + t;
+        return e < res1 ? __ldg(p.blk_kt + e) : -1;
+    };
+#pragma unroll
+    for (int i = 0; i < kStages; ++i)
+        if (i < steps) issue(i);
+    int kt = steps > 0 ? chunk_of(0) : -1;
+    if (p.w_ready) {
+        griddep_wait();
+        griddep_launch();
+    }
+
+    uint4 xr[NT][8];  // the lane's 64 activations of token 8 nt + g
+    auto load_x = [&](int kt) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const bool on = kt >= 0 && 8 * nt + g < p.M;
+            const uint4* src = reinterpret_cast<const uint4*>(p.X + (8 * nt + g) * p.ldx + 64 * (int64_t)kt);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) xr[nt][j] = on ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    load_x(kt);
+
+    float acc[4][NT][4];
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[rt][nt][c] = 0.0f;
+
+    bool alive = true;
+    for (int i = 0; i < steps; ++i) {
+        const int step = step0 + i * stride;
+        const bool valid = kt >= 0;  // this lane's columns are there
+        // activations to fp16, eight bytes per product: [pair of products][lane]
+        float back[NT][2];  // of this lane's result columns, tokens 8 nt + 2t, + 1
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float up = 1.0f, down = 1.0f;
+            if constexpr (!F16) {
+                float top = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t w[4] = {xr[nt][j].x, xr[nt][j].y, xr[nt][j].z, xr[nt][j].w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float2 f = widen2<false>(w[q]);
+                        top = max3(top, fabsf(f.x), fabsf(f.y));
+                    }
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // the largest element to [2^14, 2^15)
+                const uint32_t ex = max(__float_as_uint(top) >> 23, 15u);
+                up = __uint_as_float((268u - ex) << 23);
+                down = __uint_as_float((ex - 14u) << 23);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) back[nt][c] = __shfl_sync(0xffffffffu, down, 4 * (2 * t + c));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                uint32_t w[4] = {xr[nt][j].x, xr[nt][j].y, xr[nt][j].z, xr[nt][j].w};
+                if constexpr (!F16)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float2 f = widen2<false>(w[q]);
+                        w[q] = narrow2<true>(f.x * up, f.y * up);
+                    }
+                *reinterpret_cast<uint4*>(frag + nt * 4096 + j * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        kt = i + 1 < steps ? chunk_of(i + 1) : -1;
+        load_x(kt);
+
+        const uint32_t parity = (i / kStages) & 1u;
+        // the warp decides together; after a wait that gave up (reported) nothing is issued or waited for
+        if (__any_sync(0xffffffffu, !mbar_try_wait(&full[warp][i % kStages], parity)) && alive)
+            alive = __all_sync(0xffffffffu, mbar_wait_err(&full[warp][i % kStages], parity, p.err));
+        const uint8_t* buf = ring + (i % kStages) * kStage;
+        // scales of rows 16 rt + 8 hf + g in the lane's 64 columns: a 128-row chunk holds row
+        // r's four at (r % 32) * 16 + (r / 32) * 4. Columns past the end may hold anything: zero.
+        uint32_t sc[4][2][2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                uint2 w = *reinterpret_cast<const uint2*>(buf + kCodes + t * 512 + (16 * q + 8 * hf + g) * 16 + (tile & 1) * 8);
+                if (!valid) w = make_uint2(0, 0);
+                e4m3x4_half(w.x, sc[q][hf][0], sc[q][hf][1]);
+                e4m3x4_half(w.y, sc[q + 2][hf][0], sc[q + 2][hf][1]);
+            }
+        float cc[4][NT][4];
+        float(&sum)[4][NT][4] = F16 ? acc : cc;
+        if constexpr (!F16)
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) cc[rt][nt][c] = 0.0f;
+        // 16-byte piece h of the lane's columns in row r: swizzled rows of 128 bytes, or packed blocks
+        const bool isb = step < nbase;
+        const uint8_t* codes = isb ? buf + g * 128 : buf + t * 2048 + g * 16;
+        const int row8 = isb ? 1024 : 256;  // eight rows further
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            const uint8_t* at = codes + (isb ? ((2 * t + h) ^ g) * 16 : h * 128);
+            uint4 b[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int w = 0; w < 4; ++w) b[nt][w] = *reinterpret_cast<const uint4*>(frag + nt * 4096 + (4 * h + w) * 512 + lane * 16);
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) {
+                const uint4 a0 = *reinterpret_cast<const uint4*>(at + (2 * rt) * row8);
+                const uint4 a1 = *reinterpret_cast<const uint4*>(at + (2 * rt + 1) * row8);
+                const uint32_t s0 = h ? sc[rt][0][1] : sc[rt][0][0], s1 = h ? sc[rt][1][1] : sc[rt][1][0];
+                const uint32_t w0[4] = {a0.x, a0.y, a0.z, a0.w}, w1[4] = {a1.x, a1.y, a1.z, a1.w};
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t x[4], y[4];
+                    e2m1x8_half(w0[w], x);
+                    e2m1x8_half(w1[w], y);
+                    const __half2 f0 = w < 2 ? low2(s0) : high2(s0), f1 = w < 2 ? low2(s1) : high2(s1);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t a[4] = {mul_h2(x[2 * e], f0), mul_h2(y[2 * e], f1), mul_h2(x[2 * e + 1], f0),
+                                               mul_h2(y[2 * e + 1], f1)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_f16(sum[rt][nt], a, e ? b[nt][w].z : b[nt][w].x, e ? b[nt][w].w : b[nt][w].y);
+                    }
+                }
+            }
+        }
+        if constexpr (!F16)
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[rt][nt][c] = __fmaf_rn(cc[rt][nt][c], back[nt][c & 1], acc[rt][nt][c]);
+        __syncwarp();
+        if (i + kStages < steps && alive) issue(i + kStages);
+    }
+    if (!alive)  // the last copies get their (bounded) time
+        for (int i = max(0, steps - kStages); i < steps; ++i)
+            mbar_wait_err(&full[warp][i % kStages], (i / kStages) & 1u, p.err);
+
+    // the warps' sums, then the CTAs', each in order
+    __syncthreads();
+    float* sums = reinterpret_cast<float*>(smem);  // [warp][token][kPitch]
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                sums[(warp * 8 * NT + 8 * nt + 2 * t + (c & 1)) * kPitch + 16 * rt + g + 8 * (c >> 1)] = acc[rt][nt][c];
+    __syncthreads();
+    const float gw = __ldg(p.g_w);
+    float* mine = sums + kWarps * 8 * NT * kPitch;  // [token][kPitch], this CTA's
+    for (int i = tid; i < kRows * p.M; i += kThreads) {
+        const int m = i / kRows, n = i % kRows;
+        float v = sums[m * kPitch + n];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) v += sums[(w * 8 * NT + m) * kPitch + n];
+        if (S == 1)
+            p.Y[m * p.ldy + tile * kRows + n] = (uint16_t)narrow2<F16>(v * gw, 0.0f);
+        else
+            mine[m * kPitch + n] = v;
+    }
+    if (S > 1) {
+        cluster_sync();
+        for (int i = tid + rank * kThreads; i < kRows * p.M; i += S * kThreads) {
+            const int m = i / kRows, n = i % kRows;
+            float v = 0.0f;
+            for (int r = 0; r < S; ++r) v += ld_dsmem_f32(mine + m * kPitch + n, r);
+            p.Y[m * p.ldy + tile * kRows + n] = (uint16_t)narrow2<F16>(v * gw, 0.0f);
+        }
+        cluster_sync();  // no CTA leaves while another reads its sums
     }
 }
 
-template <int MT, bool F16>
-__global__ void __launch_bounds__(32 * kWarps) k_gemv(const GemvParams p) {
-    griddep_wait();
-    griddep_launch();
-    const int lane = threadIdx.x & 31, n = blockIdx.x * kWarps + (threadIdx.x >> 5), m0 = blockIdx.y * MT;
-    if (n >= p.N) return;
-    float acc[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[m] = 0.0f;
-    if (p.base) {
-        const uint8_t* row = p.codes + (int64_t)n * (p.K / 2);
-        for (int k0 = 32 * lane; k0 < p.K; k0 += 1024) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + k0 / 2));
-            const uint8_t* f = p.sf + sf_swz_offset(n, k0 / 16, p.K);
-            fma32<MT, F16>(p, w, e4m3_value(f[0]), e4m3_value(f[1]), k0, m0, acc);
-        }
-    }
-    if (p.blk_codes) {
-        const int lo = __ldg(p.tile_ptr + n / 64), hi = __ldg(p.tile_ptr + n / 64 + 1), r = n & 63, t = n & 127;
-        for (int e = 2 * lo + lane; e < 2 * hi; e += 32) {  // half a block row each
-            const int64_t b = e >> 1;
-            const int h = e & 1;
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.blk_codes + b * 2048 + (r / 8) * 256 + h * 128 + (r % 8) * 16));
-            const uint8_t* f = p.blk_sf + b * 512 + (t % 32) * 16 + (t / 32) * 4 + 2 * h;
-            fma32<MT, F16>(p, w, e4m3_value(f[0]), e4m3_value(f[1]), 64 * __ldg(p.blk_kt + b) + 32 * h, m0, acc);
-        }
-    }
-    const float g = __ldg(p.g_w);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xffffffffu, acc[m], o);
-        if (lane == 0 && m0 + m < p.M) p.Y[(m0 + m) * p.ldy + n] = (uint16_t)narrow2<F16>(acc[m] * g, 0.0f);
-    }
+template <int NT, bool F16>
+cudaError_t gemv_of(const CUtensorMap& tw, const GemvParams& p, int S, cudaStream_t s) {
+    static std::atomic<bool> done[64];
+    const cudaError_t e = once_per_device(done, [] {
+        return cudaFuncSetAttribute(k_gemv<NT, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<NT>());
+    });
+    if (e != cudaSuccess) return e;
+    return launch_pdl_cluster(k_gemv<NT, F16>, dim3(S, p.N / kRows), dim3(kThreads), smem_bytes<NT>(), s, dim3(S, 1, 1), tw, p);
 }
 
 }  // namespace
 
-cudaError_t launch_gemv(const GemvParams& p, bool f16, cudaStream_t s) {
-    const dim3 grid((p.N + kWarps - 1) / kWarps, (p.M + 3) / 4);
-    return f16 ? launch_pdl(k_gemv<4, true>, grid, dim3(32 * kWarps), 0, s, 1, p)
-               : launch_pdl(k_gemv<4, false>, grid, dim3(32 * kWarps), 0, s, 1, p);
+cudaError_t launch_gemv(const CUtensorMap& tw, const GemvParams& p, bool f16, cudaStream_t s) {
+    const int tiles = p.N / kRows, steps = (p.K / 64 + 3) / 4;
+    // CTAs that fill the GPU once, none without a step for each of its warps
+    const int S = std::max(1, std::min({8, kCtasPerSm * device_sms() / tiles, steps / kWarps}));
+    if (p.M <= 8) return f16 ? gemv_of<1, true>(tw, p, S, s) : gemv_of<1, false>(tw, p, S, s);
+    return f16 ? gemv_of<2, true>(tw, p, S, s) : gemv_of<2, false>(tw, p, S, s);
 }
 
 }  // namespace mq
