@@ -60,12 +60,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_gemv(const __grid_cons
         if (tid == 0) report_index(p.err);
         return;
     }
-    const int res0 = p.blk_codes ? __ldg(p.tile_ptr + tile) : 0, res1 = p.blk_codes ? __ldg(p.tile_ptr + tile + 1) : 0;
-    const int nbase = p.base ? (KC + 3) / 4 : 0, total = nbase + (res1 - res0 + 3) / 4;
-    const int step0 = rank * kWarps + warp, stride = S * kWarps;
-    const int steps = step0 < total ? (total - step0 + stride - 1) / stride : 0;
+    const int nbase = p.base ? (KC + 3) / 4 : 0, step0 = rank * kWarps + warp, stride = S * kWarps;
     uint8_t* ring = smem + warp * (kStages * kStage);
     uint8_t* frag = smem + kWarps * kStages * kStage + warp * (NT * 4096);  // this warp's activations as fp16 operands
+    int res0 = 0, res1 = 0;
 
     auto issue = [&](int i) {
         if (lane == 0) {
@@ -86,31 +84,37 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_gemv(const __grid_cons
             }
         }
     };
-    // Column chunk (64 columns) of this lane in a step, -1 past the end.
-    auto chunk_of = [&](int i) {
+    // the first base steps fly before the residual's extent is known
+    int ahead = 0;
+    while (ahead < kStages && step0 + ahead * stride < nbase) issue(ahead++);
+    if (p.blk_codes) {
+        res0 = __ldg(p.tile_ptr + tile);
+        res1 = __ldg(p.tile_ptr + tile + 1);
+    }
+    const int total = nbase + (res1 - res0 + 3) / 4;
+    const int steps = step0 < total ? (total - step0 + stride - 1) / stride : 0;
+    while (ahead < min(kStages, steps)) issue(ahead++);
+    // Column chunk c (0..3, 64 columns) of a step, -1 past the end.
+    auto chunk_of = [&](int i, int c) {
         const int step = step0 + i * stride;
-        if (step < nbase) return 4 * step + t < KC ? 4 * step + t : -1;
-        const int e = res0 + 4 * (step - nbase) + t;
+        if (step < nbase) return 4 * step + c < KC ? 4 * step + c : -1;
+        const int e = res0 + 4 * (step - nbase) + c;
         return e < res1 ? __ldg(p.blk_kt + e) : -1;
     };
-#pragma unroll
-    for (int i = 0; i < kStages; ++i)
-        if (i < steps) issue(i);
-    int kt = steps > 0 ? chunk_of(0) : -1;
+    int kt = steps > 0 ? chunk_of(0, lane >> 3) : -1;
+    // tokens past M are zeros, and stay
+    for (int i = lane; i < NT * 256; i += 32) reinterpret_cast<uint4*>(frag)[i] = make_uint4(0, 0, 0, 0);
     if (p.w_ready) {
         griddep_wait();
         griddep_launch();
     }
 
-    uint4 xr[NT][8];  // the lane's 64 activations of token 8 nt + g
+    uint4 xr[8 * NT];  // eight activations of every token: chunk lane / 8, piece lane % 8
     auto load_x = [&](int kt) {
+        const uint16_t* src = p.X + 64 * (int64_t)kt + 8 * (lane & 7);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const bool on = kt >= 0 && 8 * nt + g < p.M;
-            const uint4* src = reinterpret_cast<const uint4*>(p.X + (8 * nt + g) * p.ldx + 64 * (int64_t)kt);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) xr[nt][j] = on ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
-        }
+        for (int m = 0; m < 8 * NT; ++m)
+            if (m < p.M) xr[m] = kt >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + m * p.ldx)) : make_uint4(0, 0, 0, 0);
     };
     load_x(kt);
 
@@ -125,45 +129,34 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_gemv(const __grid_cons
     bool alive = true;
     for (int i = 0; i < steps; ++i) {
         const int step = step0 + i * stride;
-        const bool valid = kt >= 0;  // this lane's columns are there
-        // activations to fp16, eight bytes per product: [pair of products][lane]
-        float back[NT][2];  // of this lane's result columns, tokens 8 nt + 2t, + 1
+        const bool valid = step < nbase ? 4 * step + t < KC : res0 + 4 * (step - nbase) + t < res1;  // columns of this lane's rows
+        // Activations to fp16, as operands: piece j (two products) of lane l's columns at slot
+        // l ^ j, so that neither these stores nor the loads below meet in a bank.
+        float back[NT][2] = {};  // scale of this lane's result columns, tokens 8 nt + 2t, + 1
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float up = 1.0f, down = 1.0f;
+        for (int m = 0; m < 8 * NT; ++m) {
+            if (m >= p.M) continue;
+            uint32_t w[4] = {xr[m].x, xr[m].y, xr[m].z, xr[m].w};
             if constexpr (!F16) {
-                float top = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t w[4] = {xr[nt][j].x, xr[nt][j].y, xr[nt][j].z, xr[nt][j].w};
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float2 f = widen2<false>(w[q]);
-                        top = max3(top, fabsf(f.x), fabsf(f.y));
-                    }
-                }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // the largest element's bits (bf16, two at a time), over the warp
+                const uint32_t a01 = __vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu);
+                const uint32_t a = __vmaxu2(__vmaxu2(a01, w[2] & 0x7FFF7FFFu), w[3] & 0x7FFF7FFFu);
+                const uint32_t top = __reduce_max_sync(0xffffffffu, max(a & 0xFFFFu, a >> 16));
                 // the largest element to [2^14, 2^15)
-                const uint32_t ex = max(__float_as_uint(top) >> 23, 15u);
-                up = __uint_as_float((268u - ex) << 23);
-                down = __uint_as_float((ex - 14u) << 23);
+                const uint32_t ex = max(top >> 7, 15u);
+                const float up = __uint_as_float((268u - ex) << 23), down = __uint_as_float((ex - 14u) << 23);
+                if (((m & 7) >> 1) == t) back[m / 8][m & 1] = down;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) back[nt][c] = __shfl_sync(0xffffffffu, down, 4 * (2 * t + c));
+                for (int q = 0; q < 4; ++q) {
+                    const float2 f = widen2<false>(w[q]);
+                    w[q] = narrow2<true>(f.x * up, f.y * up);
+                }
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                uint32_t w[4] = {xr[nt][j].x, xr[nt][j].y, xr[nt][j].z, xr[nt][j].w};
-                if constexpr (!F16)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float2 f = widen2<false>(w[q]);
-                        w[q] = narrow2<true>(f.x * up, f.y * up);
-                    }
-                *reinterpret_cast<uint4*>(frag + nt * 4096 + j * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            const int j = lane & 7, slot = (4 * (m & 7) + (lane >> 3)) ^ j;
+            *reinterpret_cast<uint4*>(frag + (m / 8) * 4096 + j * 512 + slot * 16) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        kt = i + 1 < steps ? chunk_of(i + 1) : -1;
+        __syncwarp();
+        kt = i + 1 < steps ? chunk_of(i + 1, lane >> 3) : -1;
         load_x(kt);
 
         const uint32_t parity = (i / kStages) & 1u;
@@ -203,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_gemv(const __grid_cons
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int w = 0; w < 4; ++w) b[nt][w] = *reinterpret_cast<const uint4*>(frag + nt * 4096 + (4 * h + w) * 512 + lane * 16);
+                for (int w = 0; w < 4; ++w) b[nt][w] = *reinterpret_cast<const uint4*>(frag + nt * 4096 + (4 * h + w) * 512 + (lane ^ (4 * h + w)) * 16);
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) {
                 const uint4 a0 = *reinterpret_cast<const uint4*>(at + (2 * rt) * row8);
