@@ -88,7 +88,7 @@ mq_status mq_gemv(const void* X, mq_dtype type, int64_t ldx, const mq_nvfp4_mat*
     p.w_ready = (flags & MQ_GEMM_WEIGHTS_READY) ? 1 : 0;
     p.err = device_error_word();
     CUtensorMap tw;
-    if (!p.err || !tensor_map_bytes(&tw, wq->codes, (uint64_t)K / 2, (uint64_t)N, 128, 64)) return MQ_ERR_CUDA;
+    if (!p.err || !tensor_map_rows64(&tw, wq->codes, (uint64_t)K / 2, (uint64_t)N)) return MQ_ERR_CUDA;
     return count_launches(launch_gemv(tw, p, type == MQ_F16, as_stream(stream)), 1);
 }
 

@@ -126,13 +126,13 @@ struct AttnParams {
 // api.cu: a launch's status, counted in mq_launch_count; the current device's error word
 mq_status count_launches(cudaError_t e, int kernels);
 int* device_error_word();
-bool tensor_map_bytes(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_bytes,
-                      uint32_t box_rows);
+// a byte matrix in boxes of 64 bytes x 64 rows, not swizzled; zeros outside
+bool tensor_map_rows64(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows);
 int device_sms();  // gemm.cu: SMs of the current device (148 without one)
 
 cudaError_t launch_heads(const HeadsParams& p, int D, bool f16, cudaStream_t s);
 cudaError_t launch_kv_read(const HeadsParams& p, int D, bool f16, cudaStream_t s);
-// tw: the codes as a byte matrix in boxes of 128 bytes x 64 rows
+// tw: the codes (tensor_map_rows64)
 cudaError_t launch_gemv(const CUtensorMap& tw, const GemvParams& p, bool f16, cudaStream_t s);
 // bytes: partials, then counters at *counters_at
 size_t attn_workspace(int q_heads, int kv_heads, int D, int max_q, size_t* counters_at);
