@@ -3,11 +3,15 @@
 //
 //   u = x * (mean_d x^2 + eps)^(-1/2) * w_d,   (a, b) -> (a cos - b sin, b cos + a sin)
 //
-// Every element is read once and written once, so the floor is the bytes. A row (one head
-// of one token) is held by D/8 lanes, 16 bytes each: the sum of squares is a shuffle tree,
-// the partner of a rotated half sits rot/16 lanes away, and a group of 16 quantized
-// elements is a lane pair. A warp keeps one token and walks heads, so that the token's
-// angles (fp64: a far position times a frequency loses its fraction in fp32) are formed once.
+// Every element is read once and written once, so the floor is the bytes; few tokens are
+// bound by the launch and one chain of loads. A CTA takes a token and some of its heads. Its
+// threads form the token's angles once, one each (fp64: a far position times a frequency
+// loses its fraction in fp32), and share them. A row (one head) is held by D/8 lanes, 16
+// bytes each: the sum of squares is a shuffle tree, the partner of a rotated half sits
+// rot/16 lanes away, and a group of 16 quantized elements is a lane pair. A warp's next row is
+// in flight while it works on one.
+#include <algorithm>
+
 #include "ops.cuh"
 
 namespace mq {
@@ -15,6 +19,7 @@ namespace mq {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kSpread = 4;  // CTAs an SM that a call should have before a CTA takes a second step
 
 // The angle pos * freq in turns, its fraction in [-1/2, 1/2], then cos and sin in fp32.
 __device__ __forceinline__ float2 cos_sin(double pos, double freq) {
@@ -41,74 +46,92 @@ __device__ __forceinline__ uint32_t quantize_pair(const float (&a)[8], float g, 
                   __fmul_rn(a[5], r), __fmul_rn(a[6], r), __fmul_rn(a[7], r));
 }
 
-// One record of the cache for slot (checked by the caller) and head h.
-template <int D>
-__device__ __forceinline__ uint8_t* record_of(const CacheView& c, int64_t slot, int h) {
-    const int64_t page = slot / c.page_size;
-    const int rec = (int)(slot - page * c.page_size) >> 4;
-    return c.pages + ((page * c.heads + h) * (c.page_size >> 4) + rec) * (18 * D);
+// A slot's page and token in the page (slot checked by the caller).
+__device__ __forceinline__ void split_slot(const HeadsParams& p, int64_t slot, int64_t& page, int& token) {
+    if (slot < 0x7FFFFFFF) {
+        const uint32_t q = p.by_page.div((uint32_t)slot);
+        page = q;
+        token = (int)((uint32_t)slot - q * (uint32_t)p.cache.page_size);
+    } else {
+        page = slot / p.cache.page_size;
+        token = (int)(slot - page * p.cache.page_size);
+    }
 }
 
+// steps: how many rows a lane group walks (a CTA's rows are dealt to its warps in turn).
 template <int D, bool F16>
-__global__ void __launch_bounds__(32 * kWarps) k_heads(const HeadsParams p, int chunks, int per_warp) {
-    constexpr int LPR = D / 8, RPW = 32 / LPR;
+__global__ void __launch_bounds__(32 * kWarps) k_heads(const HeadsParams p, int steps) {
+    constexpr int LPR = D / 8, RPW = 32 / LPR, STEP = kWarps * RPW;
+    __shared__ float2 angles[D / 2];
+    const int lane = threadIdx.x & 31, li = lane % LPR, e0 = 8 * li, half = p.rot / 2;
+    const int64_t t = blockIdx.x;
+    const int nq = p.q.heads, nk = p.k.heads, nv = p.v.heads, all = nq + nk + nv;  // 0 heads: absent
+    int hg = blockIdx.y * steps * STEP + (threadIdx.x >> 5) * RPW + lane / LPR;     // this lane's row: q, k, then v heads
+    const uint16_t *qb = p.q.p + t * p.q.st + e0, *kb = p.k.p + t * p.k.st + e0, *vb = p.v.p + t * p.v.st + e0;
+    auto load = [&](int hg) {
+        if (hg >= all) return make_uint4(0, 0, 0, 0);
+        const uint16_t* src = hg < nq ? qb + hg * p.q.sh : hg < nq + nk ? kb + (hg - nq) * p.k.sh : vb + (hg - nq - nk) * p.v.sh;
+        return *reinterpret_cast<const uint4*>(src);
+    };
     griddep_wait();
     griddep_launch();
-    const int lane = threadIdx.x & 31, li = lane % LPR, sub = lane / LPR;
-    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int64_t t = unit / chunks;
-    if (t >= p.T) return;
-    const int nq = p.q.p ? p.q.heads : 0, nk = p.k.p ? p.k.heads : 0, nv = p.v.p ? p.v.heads : 0;
-    const int h0 = (int)(unit - t * chunks) * per_warp, h1 = min(h0 + per_warp, nq + nk + nv);
-    const int e0 = 8 * li, half = p.rot / 2;
-
-    // this lane's angles: of its eight elements (halves), or of its four pairs
+    uint4 next = load(hg);
+    uint8_t* rec = nullptr;  // head 0's record of this token's slot
+    int tok = 0;             // its token in the record
+    if (p.cache.pages) {
+        const int64_t slot = __ldg(p.slots + t);
+        if (slot >= (int64_t)p.cache.num_pages * p.cache.page_size) {
+            if (threadIdx.x == 0) report_index(p.err);
+        } else if (slot >= 0) {
+            int64_t page;
+            split_slot(p, slot, page, tok);
+            rec = p.cache.pages + (page * p.cache.heads * (p.cache.page_size >> 4) + (tok >> 4)) * (18 * D);
+            tok &= 15;
+        }
+    }
+    if (p.rot > 0) {
+        if ((int)threadIdx.x < half) angles[threadIdx.x] = cos_sin((double)__ldg(p.pos + t), __ldg(p.freq + threadIdx.x));
+        __syncthreads();
+    }
+    // this lane's angles: of its eight elements (halves; the sine with its sign), or of its four pairs
+    const bool turned = e0 < p.rot;
+    const int r2 = p.rot / 16, from = (lane & ~(LPR - 1)) + (li < r2 ? li + r2 : li < 2 * r2 ? li - r2 : li);
     float2 cs[8];
-    if (e0 < p.rot) {
-        const double pos = (double)__ldg(p.pos + t);
+    if (turned) {
         if (p.interleaved) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) cs[j] = cos_sin(pos, __ldg(p.freq + e0 / 2 + j));
+            for (int j = 0; j < 4; ++j) cs[j] = angles[e0 / 2 + j];
         } else {
             const int i0 = e0 < half ? e0 : e0 - half;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) cs[j] = cos_sin(pos, __ldg(p.freq + i0 + j));
-        }
-    }
-    int64_t slot = -1;
-    if (p.cache.pages) {
-        slot = __ldg(p.slots + t);
-        if (slot >= (int64_t)p.cache.num_pages * p.cache.page_size) {
-            if (lane == 0) report_index(p.err);
-            slot = -1;
-        }
-    }
-    for (int hb = h0; hb < h1; hb += RPW) {
-        const int hg = hb + sub;
-        const bool on = hg < h1;
-        const int kind = hg < nq ? 0 : hg < nq + nk ? 1 : 2;  // q, k, v
-        const HeadsView& in = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
-        const int h = kind == 0 ? hg : kind == 1 ? hg - nq : hg - nq - nk;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (on) w = *reinterpret_cast<const uint4*>(in.p + t * in.st + h * in.sh + e0);
-        float a[8];
-        {
-            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = widen2<F16>(x[j]);
-                a[2 * j] = f.x;
-                a[2 * j + 1] = f.y;
+            for (int j = 0; j < 8; ++j) {
+                cs[j] = angles[i0 + j];
+                if (e0 < half) cs[j].y = -cs[j].y;
             }
         }
+    }
+    for (int s = 0; s < steps; ++s, hg += STEP) {
+        const uint4 w = next;
+        const bool on = hg < all;
+        if (s + 1 < steps) next = load(hg + STEP);
+        const int kind = hg < nq ? 0 : hg < nq + nk ? 1 : 2;  // q, k, v
+        const int h = kind == 0 ? hg : kind == 1 ? hg - nq : hg - nq - nk;
+        uint32_t o[4] = {w.x, w.y, w.z, w.w};
+        float a[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = widen2<F16>(o[j]);
+            a[2 * j] = f.x;
+            a[2 * j + 1] = f.y;
+        }
         // the warp's rows may be of different kinds: the shuffles run for all of them
-        const uint16_t* wt = kind == 0 ? p.wq : kind == 1 ? p.wk : nullptr;
         if (p.wq || p.wk) {
             float ss = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) ss = __fmaf_rn(a[j], a[j], ss);
 #pragma unroll
-            for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            for (int x = 1; x < LPR; x <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, x);
+            const uint16_t* wt = kind == 0 ? p.wq : kind == 1 ? p.wk : nullptr;
             if (wt) {
                 const float r = rsqrtf(ss * (1.0f / D) + p.eps);
                 const uint4 g = __ldg(reinterpret_cast<const uint4*>(wt + e0));
@@ -123,7 +146,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_heads(const HeadsParams p, int 
         }
         if (p.rot > 0) {
             if (p.interleaved) {
-                if (e0 < p.rot && kind < 2) {
+                if (turned && kind < 2) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float x = a[2 * j], y = a[2 * j + 1];
@@ -132,22 +155,19 @@ __global__ void __launch_bounds__(32 * kWarps) k_heads(const HeadsParams p, int 
                     }
                 }
             } else {
-                const int r2 = p.rot / 16;
-                const int src = sub * LPR + (li < r2 ? li + r2 : li < 2 * r2 ? li - r2 : li);
-                const float sign = li < r2 ? -1.0f : 1.0f;
+                float y[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float y = __shfl_sync(0xffffffffu, a[j], src);
-                    if (e0 < p.rot && kind < 2) a[j] = __fmaf_rn(a[j], cs[j].x, sign * y * cs[j].y);
-                }
+                for (int j = 0; j < 8; ++j) y[j] = __shfl_sync(0xffffffffu, a[j], from);
+                if (turned && kind < 2)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) a[j] = __fmaf_rn(a[j], cs[j].x, y[j] * cs[j].y);
             }
         }
-        uint32_t o[4];
+        if (kind < 2) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = narrow2<F16>(a[2 * j], a[2 * j + 1]);
-        if (kind < 2 && on) {
+            for (int j = 0; j < 4; ++j) o[j] = narrow2<F16>(a[2 * j], a[2 * j + 1]);
             const HeadsView& out = kind == 0 ? p.qo : p.ko;
-            if (out.p)
+            if (on && out.p)
                 *reinterpret_cast<uint4*>(out.p + t * out.st + h * out.sh + e0) = make_uint4(o[0], o[1], o[2], o[3]);
         }
         if constexpr (D <= 128) {
@@ -163,69 +183,75 @@ __global__ void __launch_bounds__(32 * kWarps) k_heads(const HeadsParams p, int 
                 const float g = (sc && on && kind > 0) ? __ldg(sc + h) : 1.0f;
                 uint32_t sf;
                 const uint32_t codes = quantize_pair(a, g, __fmul_rn(6.0f, g), sf);
-                if (on && kind > 0 && slot >= 0) {
-                    uint8_t* rec = record_of<D>(p.cache, slot, h);
-                    const int i = (int)(slot & 15), q = li >> 1;  // page_size is a multiple of 16
-                    const int at = kind == 1 ? i * (D / 2) + 4 * li : rec_vcodes<D>(i, q) + 4 * (li & 1);
-                    *reinterpret_cast<uint32_t*>(rec + at) = codes;
-                    if (!(li & 1)) rec[kind == 1 ? rec_kscale<D>(i, q) : rec_vscale<D>(i, q)] = (uint8_t)sf;
+                if (on && kind > 0 && rec) {
+                    uint8_t* r = rec + (int64_t)h * ((p.cache.page_size >> 4) * (18 * D));
+                    const int q = li >> 1;
+                    const int at = kind == 1 ? tok * (D / 2) + 4 * li : rec_vcodes<D>(tok, q) + 4 * (li & 1);
+                    *reinterpret_cast<uint32_t*>(r + at) = codes;
+                    if (!(li & 1)) r[kind == 1 ? rec_kscale<D>(tok, q) : rec_vscale<D>(tok, q)] = (uint8_t)sf;
                 }
             }
         }
     }
 }
 
-// The cached rows of slots[t]: warp per (token, heads), lanes as above.
+// The cached rows of slots[t], lanes and warps as above; two of a warp's rows at a time.
 template <int D, bool F16>
 __global__ void __launch_bounds__(32 * kWarps) k_kv_read(const HeadsParams p) {
-    constexpr int LPR = D / 8, RPW = 32 / LPR;
+    constexpr int LPR = D / 8, RPW = 32 / LPR, STEP = kWarps * RPW;
+    const int lane = threadIdx.x & 31, li = lane % LPR, q = li >> 1;
+    const int64_t t = blockIdx.x;
+    const int H = p.cache.heads;
     griddep_wait();
     griddep_launch();
-    const int lane = threadIdx.x & 31, li = lane % LPR, sub = lane / LPR;
-    const int H = p.cache.heads, rows = 2 * H;
-    const int64_t row = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * RPW + sub;
-    const int64_t t = row / rows;
-    if (t >= p.T) return;
-    const int hg = (int)(row - t * rows), kind = hg >= H, h = kind ? hg - H : hg;
     const int64_t slot = __ldg(p.slots + t);
     if (slot < 0) return;
     if (slot >= (int64_t)p.cache.num_pages * p.cache.page_size) {
-        if (li == 0) report_index(p.err);
+        if (threadIdx.x == 0) report_index(p.err);
         return;
     }
-    const uint8_t* rec = record_of<D>(p.cache, slot, h);
-    const int i = (int)(slot & 15), q = li >> 1;
-    const float* sc = kind ? p.cache.v_scale : p.cache.k_scale;
-    const float g = sc ? __ldg(sc + h) : 1.0f;
-    const uint32_t codes =
-        *reinterpret_cast<const uint32_t*>(rec + (kind ? rec_vcodes<D>(i, q) + 4 * (li & 1) : i * (D / 2) + 4 * li));
-    const float d = __fmul_rn(e4m3_value(rec[kind ? rec_vscale<D>(i, q) : rec_kscale<D>(i, q)]), g);
-    float v[8];
-    e2m1x8_values(codes, v);
-    uint32_t o[4];
+    int64_t page;
+    int tok;
+    split_slot(p, slot, page, tok);
+    const int64_t per_head = (int64_t)(p.cache.page_size >> 4) * (18 * D);
+    const uint8_t* rec = p.cache.pages + page * H * per_head + (tok >> 4) * (18 * D);
+    tok &= 15;
+    const int kat = tok * (D / 2) + 4 * li, vat = rec_vcodes<D>(tok, q) + 4 * (li & 1);
+    const int ksat = rec_kscale<D>(tok, q), vsat = rec_vscale<D>(tok, q);
+    uint16_t *kb = p.k.p + t * p.k.st + 8 * li, *vb = p.v.p + t * p.v.st + 8 * li;
+    for (int h = (threadIdx.x >> 5) * RPW + lane / LPR; h < H; h += STEP) {
+        const uint8_t* r = rec + h * per_head;
+        const uint32_t kc = *reinterpret_cast<const uint32_t*>(r + kat), vc = *reinterpret_cast<const uint32_t*>(r + vat);
+        const uint32_t ks = r[ksat], vs = r[vsat];
+        const float gk = p.cache.k_scale ? __ldg(p.cache.k_scale + h) : 1.0f;
+        const float gv = p.cache.v_scale ? __ldg(p.cache.v_scale + h) : 1.0f;
+        auto put = [&](uint32_t codes, uint32_t sf, float g, uint16_t* dst) {
+            const float d = __fmul_rn(e4m3_value(sf), g);
+            float v[8];
+            e2m1x8_values(codes, v);
+            uint32_t o[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = narrow2<F16>(__fmul_rn(v[2 * j], d), __fmul_rn(v[2 * j + 1], d));
-    const HeadsView& out = kind ? p.v : p.k;
-    *reinterpret_cast<uint4*>(out.p + t * out.st + h * out.sh + 8 * li) = make_uint4(o[0], o[1], o[2], o[3]);
+            for (int j = 0; j < 4; ++j) o[j] = narrow2<F16>(__fmul_rn(v[2 * j], d), __fmul_rn(v[2 * j + 1], d));
+            *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+        };
+        put(kc, ks, gk, kb + h * p.k.sh);
+        put(vc, vs, gv, vb + h * p.v.sh);
+    }
 }
 
 template <int D, bool F16>
 cudaError_t heads_of(const HeadsParams& p, cudaStream_t s) {
-    constexpr int RPW = 32 / (D / 8);
-    const int heads = (p.q.p ? p.q.heads : 0) + (p.k.p ? p.k.heads : 0) + (p.v.p ? p.v.heads : 0);
-    const int per = RPW * 4;  // heads a warp walks
-    const int chunks = (heads + per - 1) / per;
-    const int64_t blocks = ((int64_t)p.T * chunks + kWarps - 1) / kWarps;
-    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    return launch_pdl(k_heads<D, F16>, dim3((unsigned)blocks), dim3(32 * kWarps), 0, s, 1, p, chunks, per);
+    constexpr int STEP = kWarps * (32 / (D / 8));  // rows of a CTA at a time
+    const int steps_all = (p.q.heads + p.k.heads + p.v.heads + STEP - 1) / STEP;
+    // few tokens: their heads are spread over more CTAs, down to one step each
+    const int spread = (int)std::min<int64_t>(steps_all, std::max<int64_t>(1, (int64_t)kSpread * device_sms() / p.T));
+    const int steps = (steps_all + spread - 1) / spread;
+    return launch_pdl(k_heads<D, F16>, dim3((unsigned)p.T, (steps_all + steps - 1) / steps), dim3(32 * kWarps), 0, s, 1, p, steps);
 }
 
 template <int D, bool F16>
 cudaError_t read_of(const HeadsParams& p, cudaStream_t s) {
-    constexpr int rows_per_block = kWarps * (32 / (D / 8));
-    const int64_t blocks = ((int64_t)p.T * 2 * p.cache.heads + rows_per_block - 1) / rows_per_block;
-    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    return launch_pdl(k_kv_read<D, F16>, dim3((unsigned)blocks), dim3(32 * kWarps), 0, s, 1, p);
+    return launch_pdl(k_kv_read<D, F16>, dim3((unsigned)p.T), dim3(32 * kWarps), 0, s, 1, p);
 }
 
 }  // namespace

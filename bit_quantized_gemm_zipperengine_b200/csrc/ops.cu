@@ -121,6 +121,7 @@ static mq_status heads_impl(const mq_heads* q, const mq_heads* k, const mq_heads
     p.interleaved = interleaved ? 1 : 0;
     p.slots = slots;
     p.cache = view(cache);
+    p.by_page = FastDiv(cache ? cache->page_size : 1);
     p.err = device_error_word();
     if (!p.err) return MQ_ERR_CUDA;
     return count_launches(launch_heads(p, D, type == MQ_F16, as_stream(stream)), 1);
@@ -164,6 +165,7 @@ mq_status mq_kv_read(const mq_kv_cache* cache, const int64_t* slots, int T, cons
     p.T = T;
     p.slots = slots;
     p.cache = view(cache);
+    p.by_page = FastDiv(cache ? cache->page_size : 1);
     p.err = device_error_word();
     if (!p.err) return MQ_ERR_CUDA;
     return count_launches(launch_kv_read(p, cache->D, type == MQ_F16, as_stream(stream)), 1);

@@ -63,6 +63,20 @@ __device__ __forceinline__ int rec_vscale(int i, int q) {
 // Records an index that a kernel found out of range in the device error word.
 __device__ __forceinline__ void report_index(int* err) { atomicCAS(err, 0, (int)MQ_ERR_INVALID_ARG); }
 
+// Division of n < 2^31 by d >= 1, d known on the host: a multiply and a shift (Granlund and
+// Montgomery's round-up method).
+struct FastDiv {
+    int d;
+    uint32_t mul;
+    int shift;
+    FastDiv() = default;
+    explicit FastDiv(int divisor) : d(divisor), shift(0) {
+        while ((int64_t(1) << shift) < d) ++shift;
+        mul = (uint32_t)(((uint64_t(1) << 32) * ((uint64_t(1) << shift) - (uint64_t)d)) / (uint64_t)d + 1);
+    }
+    __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
 struct HeadsParams {
     HeadsView q, k, v, qo, ko;  // p == null: absent
     int T;
@@ -74,6 +88,7 @@ struct HeadsParams {
     const int64_t* slots;       // with a cache
     CacheView cache;            // pages == null: none
     int* err;
+    FastDiv by_page;            // tokens of a page
 };
 
 struct GemvParams {
@@ -89,20 +104,6 @@ struct GemvParams {
     int base;     // 0: the residual alone
     int w_ready;  // the weight was complete before this kernel could start
     int* err;
-};
-
-// Division of n < 2^31 by d >= 1, d known on the host: a multiply and a shift (Granlund and
-// Montgomery's round-up method).
-struct FastDiv {
-    int d;
-    uint32_t mul;
-    int shift;
-    FastDiv() = default;
-    explicit FastDiv(int divisor) : d(divisor), shift(0) {
-        while ((int64_t(1) << shift) < d) ++shift;
-        mul = (uint32_t)(((uint64_t(1) << 32) * ((uint64_t(1) << shift) - (uint64_t)d)) / (uint64_t)d + 1);
-    }
-    __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
 };
 
 struct AttnParams {
