@@ -18,7 +18,10 @@ namespace mq {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 2;
+constexpr int kUnroll = 2;  // rows a lane group works on together
+constexpr int kReadWarps = 2;
+constexpr int kReadUnroll = 2;
 constexpr int kSpread = 4;  // CTAs an SM that a call should have before a CTA takes a second step
 
 // The angle pos * freq in turns, its fraction in [-1/2, 1/2], then cos and sin in fp32.
@@ -58,24 +61,52 @@ __device__ __forceinline__ void split_slot(const HeadsParams& p, int64_t slot, i
     }
 }
 
-// steps: how many rows a lane group walks (a CTA's rows are dealt to its warps in turn).
-template <int D, bool F16>
-__global__ void __launch_bounds__(32 * kWarps) k_heads(const HeadsParams p, int steps) {
-    constexpr int LPR = D / 8, RPW = 32 / LPR, STEP = kWarps * RPW;
-    __shared__ float2 angles[D / 2];
+// How the heads of a call are dealt: kWarps * RPW * kUnroll rows of one kind (q, k, v) a
+// step, steps numbered through the kinds; a CTA takes `steps` of them.
+struct Deal {
+    int q, k, v;  // steps of each kind
+    int steps;
+};
+
+// TURN: 0 none, 1 halves, 2 interleaved pairs.
+template <int D, bool F16, int TURN>
+__global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) k_heads(const HeadsParams p, const Deal deal) {
+    constexpr int LPR = D / 8, RPW = 32 / LPR, STEP = kWarps * RPW * kUnroll;
+    __shared__ float2 angles[TURN ? D / 2 : 1];
     const int lane = threadIdx.x & 31, li = lane % LPR, e0 = 8 * li, half = p.rot / 2;
+    const int row = (threadIdx.x >> 5) * RPW + lane / LPR;  // of a step's rows: this one and kUnroll - 1 more, kWarps * RPW apart
     const int64_t t = blockIdx.x;
-    const int nq = p.q.heads, nk = p.k.heads, nv = p.v.heads, all = nq + nk + nv;  // 0 heads: absent
-    int hg = blockIdx.y * steps * STEP + (threadIdx.x >> 5) * RPW + lane / LPR;     // this lane's row: q, k, then v heads
-    const uint16_t *qb = p.q.p + t * p.q.st + e0, *kb = p.k.p + t * p.k.st + e0, *vb = p.v.p + t * p.v.st + e0;
-    auto load = [&](int hg) {
-        if (hg >= all) return make_uint4(0, 0, 0, 0);
-        const uint16_t* src = hg < nq ? qb + hg * p.q.sh : hg < nq + nk ? kb + (hg - nq) * p.k.sh : vb + (hg - nq - nk) * p.v.sh;
-        return *reinterpret_cast<const uint4*>(src);
+    int s = blockIdx.y * deal.steps;
+    const int s1 = min(s + deal.steps, deal.q + deal.k + deal.v);
+
+    // one step's kind, first head and operands (the same for the whole CTA)
+    struct Kind {
+        int kind, h0, heads;
+        const uint16_t* src;
+        int64_t sh;
+    };
+    auto kind_of = [&](int s) {
+        Kind k;
+        k.kind = s < deal.q ? 0 : s < deal.q + deal.k ? 1 : 2;
+        const HeadsView& in = k.kind == 0 ? p.q : k.kind == 1 ? p.k : p.v;
+        k.h0 = (s - (k.kind == 0 ? 0 : k.kind == 1 ? deal.q : deal.q + deal.k)) * STEP;
+        k.heads = in.heads;
+        k.src = in.p + t * in.st;
+        k.sh = in.sh;
+        return k;
+    };
+    uint4 next[kUnroll];
+    auto load = [&](const Kind& k) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int h = k.h0 + row + u * (kWarps * RPW);
+            next[u] = h < k.heads ? *reinterpret_cast<const uint4*>(k.src + h * k.sh + e0) : make_uint4(0, 0, 0, 0);
+        }
     };
     griddep_wait();
     griddep_launch();
-    uint4 next = load(hg);
+    Kind k = kind_of(s);
+    load(k);
     uint8_t* rec = nullptr;  // head 0's record of this token's slot
     int tok = 0;             // its token in the record
     if (p.cache.pages) {
@@ -89,116 +120,114 @@ __global__ void __launch_bounds__(32 * kWarps) k_heads(const HeadsParams p, int 
             tok &= 15;
         }
     }
-    if (p.rot > 0) {
-        if ((int)threadIdx.x < half) angles[threadIdx.x] = cos_sin((double)__ldg(p.pos + t), __ldg(p.freq + threadIdx.x));
-        __syncthreads();
-    }
-    // this lane's angles: of its eight elements (halves; the sine with its sign), or of its four pairs
-    const bool turned = e0 < p.rot;
-    const int r2 = p.rot / 16, from = (lane & ~(LPR - 1)) + (li < r2 ? li + r2 : li < 2 * r2 ? li - r2 : li);
+    // this lane's angles: of its eight elements (halves; the sine with its sign), or of its four
+    // pairs; a lane past the rotation turns by nothing
     float2 cs[8];
-    if (turned) {
-        if (p.interleaved) {
+    const int r2 = p.rot / 16, from = (lane & ~(LPR - 1)) + (li < r2 ? li + r2 : li < 2 * r2 ? li - r2 : li);
+    if constexpr (TURN != 0) {
+        const double pos = (double)__ldg(p.pos + t);
+        for (int i = threadIdx.x; i < half; i += 32 * kWarps) angles[i] = cos_sin(pos, __ldg(p.freq + i));
+        __syncthreads();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) cs[j] = angles[e0 / 2 + j];
-        } else {
-            const int i0 = e0 < half ? e0 : e0 - half;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                cs[j] = angles[i0 + j];
-                if (e0 < half) cs[j].y = -cs[j].y;
+        for (int j = 0; j < (TURN == 2 ? 4 : 8); ++j) {
+            cs[j] = make_float2(1.0f, 0.0f);
+            if (e0 < p.rot) {
+                cs[j] = angles[TURN == 2 ? e0 / 2 + j : e0 < half ? e0 + j : e0 - half + j];
+                if (TURN == 1 && e0 < half) cs[j].y = -cs[j].y;
             }
         }
     }
-    for (int s = 0; s < steps; ++s, hg += STEP) {
-        const uint4 w = next;
-        const bool on = hg < all;
-        if (s + 1 < steps) next = load(hg + STEP);
-        const int kind = hg < nq ? 0 : hg < nq + nk ? 1 : 2;  // q, k, v
-        const int h = kind == 0 ? hg : kind == 1 ? hg - nq : hg - nq - nk;
-        uint32_t o[4] = {w.x, w.y, w.z, w.w};
-        float a[8];
+    for (; s < s1; ++s) {
+        const Kind c = k;
+        uint4 w[kUnroll];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 f = widen2<F16>(o[j]);
-            a[2 * j] = f.x;
-            a[2 * j + 1] = f.y;
+        for (int u = 0; u < kUnroll; ++u) w[u] = next[u];
+        if (s + 1 < s1) {
+            k = kind_of(s + 1);
+            load(k);
         }
-        // the warp's rows may be of different kinds: the shuffles run for all of them
-        if (p.wq || p.wk) {
-            float ss = 0.0f;
+        const uint16_t* wt = c.kind == 0 ? p.wq : c.kind == 1 ? p.wk : nullptr;
+        const HeadsView& out = c.kind == 0 ? p.qo : p.ko;
+        const bool store = c.kind < 2 && out.p, quantize = c.kind > 0 && p.cache.pages;
+        uint16_t* dst = out.p + t * out.st + e0;
+        const float* sc = c.kind == 1 ? p.cache.k_scale : p.cache.v_scale;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ss = __fmaf_rn(a[j], a[j], ss);
-#pragma unroll
-            for (int x = 1; x < LPR; x <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, x);
-            const uint16_t* wt = kind == 0 ? p.wq : kind == 1 ? p.wk : nullptr;
-            if (wt) {
-                const float r = rsqrtf(ss * (1.0f / D) + p.eps);
-                const uint4 g = __ldg(reinterpret_cast<const uint4*>(wt + e0));
-                const uint32_t x[4] = {g.x, g.y, g.z, g.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 f = widen2<F16>(x[j]);
-                    a[2 * j] *= r * f.x;
-                    a[2 * j + 1] *= r * f.y;
-                }
-            }
-        }
-        if (p.rot > 0) {
-            if (p.interleaved) {
-                if (turned && kind < 2) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float x = a[2 * j], y = a[2 * j + 1];
-                        a[2 * j] = __fmaf_rn(x, cs[j].x, -(y * cs[j].y));
-                        a[2 * j + 1] = __fmaf_rn(y, cs[j].x, x * cs[j].y);
-                    }
-                }
-            } else {
-                float y[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = __shfl_sync(0xffffffffu, a[j], from);
-                if (turned && kind < 2)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) a[j] = __fmaf_rn(a[j], cs[j].x, y[j] * cs[j].y);
-            }
-        }
-        if (kind < 2) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] = narrow2<F16>(a[2 * j], a[2 * j + 1]);
-            const HeadsView& out = kind == 0 ? p.qo : p.ko;
-            if (on && out.p)
-                *reinterpret_cast<uint4*>(out.p + t * out.st + h * out.sh + e0) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-        if constexpr (D <= 128) {
-            if (p.cache.pages) {
-                // what the cache holds is the rounded row
+        for (int u = 0; u < kUnroll; ++u) {
+            const int h = c.h0 + row + u * (kWarps * RPW);
+            const bool on = h < c.heads;
+            uint32_t o[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+            float a[8];
+            if (c.kind < 2) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float2 f = widen2<F16>(o[j]);
                     a[2 * j] = f.x;
                     a[2 * j + 1] = f.y;
                 }
-                const float* sc = kind == 1 ? p.cache.k_scale : p.cache.v_scale;
-                const float g = (sc && on && kind > 0) ? __ldg(sc + h) : 1.0f;
-                uint32_t sf;
-                const uint32_t codes = quantize_pair(a, g, __fmul_rn(6.0f, g), sf);
-                if (on && kind > 0 && rec) {
-                    uint8_t* r = rec + (int64_t)h * ((p.cache.page_size >> 4) * (18 * D));
-                    const int q = li >> 1;
-                    const int at = kind == 1 ? tok * (D / 2) + 4 * li : rec_vcodes<D>(tok, q) + 4 * (li & 1);
-                    *reinterpret_cast<uint32_t*>(r + at) = codes;
-                    if (!(li & 1)) r[kind == 1 ? rec_kscale<D>(tok, q) : rec_vscale<D>(tok, q)] = (uint8_t)sf;
+                if (wt) {
+                    float ss = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) ss = __fmaf_rn(a[j], a[j], ss);
+#pragma unroll
+                    for (int x = 1; x < LPR; x <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, x);
+                    const float r = rsqrtf(ss * (1.0f / D) + p.eps);
+                    const uint4 g = __ldg(reinterpret_cast<const uint4*>(wt + e0));
+                    const uint32_t x[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 f = widen2<F16>(x[j]);
+                        a[2 * j] *= r * f.x;
+                        a[2 * j + 1] *= r * f.y;
+                    }
+                }
+                if constexpr (TURN == 2) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float x = a[2 * j], y = a[2 * j + 1];
+                        a[2 * j] = __fmaf_rn(x, cs[j].x, -(y * cs[j].y));
+                        a[2 * j + 1] = __fmaf_rn(y, cs[j].x, x * cs[j].y);
+                    }
+                } else if constexpr (TURN == 1) {
+                    float y[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[j] = __shfl_sync(0xffffffffu, a[j], from);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) a[j] = __fmaf_rn(a[j], cs[j].x, y[j] * cs[j].y);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[j] = narrow2<F16>(a[2 * j], a[2 * j + 1]);
+                if (store && on) *reinterpret_cast<uint4*>(dst + h * out.sh) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            if constexpr (D <= 128) {
+                if (quantize) {
+                    // what the cache holds is the rounded row
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 f = widen2<F16>(o[j]);
+                        a[2 * j] = f.x;
+                        a[2 * j + 1] = f.y;
+                    }
+                    const float g = sc && on ? __ldg(sc + h) : 1.0f;
+                    uint32_t sf;
+                    const uint32_t codes = quantize_pair(a, g, __fmul_rn(6.0f, g), sf);
+                    if (on && rec) {
+                        uint8_t* r = rec + (int64_t)h * ((p.cache.page_size >> 4) * (18 * D));
+                        const int q = li >> 1;
+                        const int at = c.kind == 1 ? tok * (D / 2) + 4 * li : rec_vcodes<D>(tok, q) + 4 * (li & 1);
+                        *reinterpret_cast<uint32_t*>(r + at) = codes;
+                        if (!(li & 1)) r[c.kind == 1 ? rec_kscale<D>(tok, q) : rec_vscale<D>(tok, q)] = (uint8_t)sf;
+                    }
                 }
             }
         }
     }
 }
 
-// The cached rows of slots[t], lanes and warps as above; two of a warp's rows at a time.
+// The cached rows of slots[t], lanes and warps as above; a lane group fetches kReadUnroll heads' keys
+// and values together.
 template <int D, bool F16>
-__global__ void __launch_bounds__(32 * kWarps) k_kv_read(const HeadsParams p) {
-    constexpr int LPR = D / 8, RPW = 32 / LPR, STEP = kWarps * RPW;
+__global__ void __launch_bounds__(32 * kReadWarps) k_kv_read(const HeadsParams p) {
+    constexpr int LPR = D / 8, RPW = 32 / LPR, STEP = kReadWarps * RPW;
     const int lane = threadIdx.x & 31, li = lane % LPR, q = li >> 1;
     const int64_t t = blockIdx.x;
     const int H = p.cache.heads;
@@ -219,39 +248,59 @@ __global__ void __launch_bounds__(32 * kWarps) k_kv_read(const HeadsParams p) {
     const int kat = tok * (D / 2) + 4 * li, vat = rec_vcodes<D>(tok, q) + 4 * (li & 1);
     const int ksat = rec_kscale<D>(tok, q), vsat = rec_vscale<D>(tok, q);
     uint16_t *kb = p.k.p + t * p.k.st + 8 * li, *vb = p.v.p + t * p.v.st + 8 * li;
-    for (int h = (threadIdx.x >> 5) * RPW + lane / LPR; h < H; h += STEP) {
-        const uint8_t* r = rec + h * per_head;
-        const uint32_t kc = *reinterpret_cast<const uint32_t*>(r + kat), vc = *reinterpret_cast<const uint32_t*>(r + vat);
-        const uint32_t ks = r[ksat], vs = r[vsat];
-        const float gk = p.cache.k_scale ? __ldg(p.cache.k_scale + h) : 1.0f;
-        const float gv = p.cache.v_scale ? __ldg(p.cache.v_scale + h) : 1.0f;
-        auto put = [&](uint32_t codes, uint32_t sf, float g, uint16_t* dst) {
-            const float d = __fmul_rn(e4m3_value(sf), g);
-            float v[8];
-            e2m1x8_values(codes, v);
-            uint32_t o[4];
+    auto put = [](uint32_t codes, uint32_t sf, float g, uint16_t* dst) {
+        const float d = __fmul_rn(e4m3_value(sf), g);
+        float v[8];
+        e2m1x8_values(codes, v);
+        uint32_t o[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] = narrow2<F16>(__fmul_rn(v[2 * j], d), __fmul_rn(v[2 * j + 1], d));
-            *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-        };
-        put(kc, ks, gk, kb + h * p.k.sh);
-        put(vc, vs, gv, vb + h * p.v.sh);
+        for (int j = 0; j < 4; ++j) o[j] = narrow2<F16>(__fmul_rn(v[2 * j], d), __fmul_rn(v[2 * j + 1], d));
+        *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+    };
+    for (int h0 = (threadIdx.x >> 5) * RPW + lane / LPR; h0 < H; h0 += STEP * kReadUnroll) {
+        uint32_t kc[kReadUnroll], vc[kReadUnroll], ks[kReadUnroll], vs[kReadUnroll];
+        float gk[kReadUnroll], gv[kReadUnroll];
+#pragma unroll
+        for (int u = 0; u < kReadUnroll; ++u) {
+            const int h = min(h0 + u * STEP, H - 1);
+            const uint8_t* r = rec + h * per_head;
+            kc[u] = *reinterpret_cast<const uint32_t*>(r + kat);
+            vc[u] = *reinterpret_cast<const uint32_t*>(r + vat);
+            ks[u] = r[ksat];
+            vs[u] = r[vsat];
+            gk[u] = p.cache.k_scale ? __ldg(p.cache.k_scale + h) : 1.0f;
+            gv[u] = p.cache.v_scale ? __ldg(p.cache.v_scale + h) : 1.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < kReadUnroll; ++u) {
+            const int h = h0 + u * STEP;
+            if (h >= H) break;
+            put(kc[u], ks[u], gk[u], kb + h * p.k.sh);
+            put(vc[u], vs[u], gv[u], vb + h * p.v.sh);
+        }
     }
 }
 
 template <int D, bool F16>
 cudaError_t heads_of(const HeadsParams& p, cudaStream_t s) {
-    constexpr int STEP = kWarps * (32 / (D / 8));  // rows of a CTA at a time
-    const int steps_all = (p.q.heads + p.k.heads + p.v.heads + STEP - 1) / STEP;
+    constexpr int STEP = kWarps * (32 / (D / 8)) * kUnroll;
+    Deal d;
+    d.q = (p.q.heads + STEP - 1) / STEP;
+    d.k = (p.k.heads + STEP - 1) / STEP;
+    d.v = (p.v.heads + STEP - 1) / STEP;
     // few tokens: their heads are spread over more CTAs, down to one step each
-    const int spread = (int)std::min<int64_t>(steps_all, std::max<int64_t>(1, (int64_t)kSpread * device_sms() / p.T));
-    const int steps = (steps_all + spread - 1) / spread;
-    return launch_pdl(k_heads<D, F16>, dim3((unsigned)p.T, (steps_all + steps - 1) / steps), dim3(32 * kWarps), 0, s, 1, p, steps);
+    const int all = d.q + d.k + d.v;
+    const int spread = (int)std::min<int64_t>(all, std::max<int64_t>(1, (int64_t)kSpread * device_sms() / p.T));
+    d.steps = (all + spread - 1) / spread;
+    const dim3 grid((unsigned)p.T, (all + d.steps - 1) / d.steps), block(32 * kWarps);
+    if (p.rot == 0) return launch_pdl(k_heads<D, F16, 0>, grid, block, 0, s, 1, p, d);
+    return p.interleaved ? launch_pdl(k_heads<D, F16, 2>, grid, block, 0, s, 1, p, d)
+                         : launch_pdl(k_heads<D, F16, 1>, grid, block, 0, s, 1, p, d);
 }
 
 template <int D, bool F16>
 cudaError_t read_of(const HeadsParams& p, cudaStream_t s) {
-    return launch_pdl(k_kv_read<D, F16>, dim3((unsigned)p.T), dim3(32 * kWarps), 0, s, 1, p);
+    return launch_pdl(k_kv_read<D, F16>, dim3((unsigned)p.T), dim3(32 * kReadWarps), 0, s, 1, p);
 }
 
 }  // namespace

@@ -7,7 +7,10 @@ library or a non-CUDA tensor raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
+import threading
 
 import torch
 
@@ -349,76 +352,60 @@ def gemm_workspace(M: int, N: int, K: int, flags: int, device) -> torch.Tensor |
 _TYPES = {torch.bfloat16: MQ_BF16, torch.float16: MQ_F16}
 
 
-class _on:
-    """The call's stream as an integer, with the tensors' device current inside the block
-    (a launch on another device's stream would fail). Without a stream argument: that
-    device's current stream."""
+class _Scratch(threading.local):
+    """Five mq_heads that a call fills and the C side has read when the call returns."""
 
-    __slots__ = ("dev", "back", "stream")
-
-    def __init__(self, t: torch.Tensor, stream=None):
-        if not t.is_cuda:
-            raise MosaicError("libmosaic takes CUDA tensors only")
-        self.dev = t.get_device()
-        self.stream = (torch._C._cuda_getCurrentRawStream(self.dev) if stream is None else stream.cuda_stream)
-
-    def __enter__(self):
-        here = torch.cuda.current_device()
-        self.back = None
-        if here != self.dev:
-            self.back = here
-            torch.cuda.set_device(self.dev)
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
-        return False
+    def __init__(self):
+        self.buf = (ctypes.c_int64 * 20)()
+        self.at = [ctypes.addressof(self.buf) + 32 * i for i in range(5)]
+        self.put = [functools.partial(struct.Struct("4q").pack_into, self.buf, 32 * i) for i in range(5)]
 
 
-def _type(t: torch.Tensor, *others) -> int:
-    """The mq_dtype of 16-bit tensors, all of one type and device."""
+_scratch = _Scratch()
+
+
+def _kind(t: torch.Tensor) -> int:
+    """The mq_dtype of a 16-bit CUDA tensor."""
     code = _TYPES.get(t.dtype)
     if code is None:
         raise MosaicError(f"bf16 or fp16 tensors are taken, not {t.dtype}")
-    for o in others:
-        if o is not None and (o.dtype != t.dtype or o.device != t.device):
-            raise MosaicError(f"one type and device per call: {t.dtype} on {t.device} and {o.dtype} on {o.device}")
+    if not t.is_cuda:
+        raise MosaicError("libmosaic takes CUDA tensors only")
     return code
 
 
-def _index(t: torch.Tensor, dtype, numel: int, like: torch.Tensor, what: str) -> int:
-    """Pointer of a contiguous index array of at least numel elements."""
-    if t.dtype != dtype or t.device != like.device or t.numel() < numel or not t.is_contiguous():
-        raise MosaicError(f"{what}: {numel} contiguous {dtype} values on {like.device} are wanted, got {t.dtype} "
+def _put(i: int, t, T: int, D: int, dtype, dev: int):
+    """Address of mq_heads i, filled from t [T][heads][D] (None: None)."""
+    if t is None:
+        return None
+    n, h, d = t.shape
+    st, sh, sd = t.stride()
+    if n != T or d != D or sd != 1 or t.dtype != dtype or t.get_device() != dev:
+        raise MosaicError(f"[{T}][heads][{D}] of {dtype} on cuda:{dev} with adjacent elements is wanted, got shape "
+                          f"{tuple(t.shape)}, strides {t.stride()}, {t.dtype} on {t.device}")
+    _scratch.put[i](t.data_ptr(), h, st, sh)
+    return _scratch.at[i]
+
+
+def _index(t: torch.Tensor, dtype, numel: int, dev: int, what: str) -> int:
+    """Pointer of a contiguous array of at least numel elements on cuda:dev."""
+    if t.dtype != dtype or t.get_device() != dev or t.numel() < numel or not t.is_contiguous():
+        raise MosaicError(f"{what}: {numel} contiguous {dtype} values on cuda:{dev} are wanted, got {t.dtype} "
                           f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-class _heads:
-    """The mq_heads of several [T][heads][D] tensors in one block of memory; at(i) is the
-    address of the i-th (None for an absent one)."""
-
-    __slots__ = ("buf", "base", "have")
-
-    def __init__(self, T: int, D: int, *ts):
-        v = []
-        for t in ts:
-            if t is None:
-                v += (0, 0, 0, 0)
-                continue
-            n, h, d = t.shape
-            st, sh, sd = t.stride()
-            if n != T or d != D or sd != 1:
-                raise MosaicError(f"[{T}][heads][{D}] with adjacent elements is wanted, got shape {tuple(t.shape)}, "
-                                  f"strides {t.stride()}")
-            v += (t.data_ptr(), h, st, sh)
-        self.buf = (ctypes.c_int64 * len(v))(*v)
-        self.base = ctypes.addressof(self.buf)
-        self.have = [t is not None for t in ts]
-
-    def at(self, i: int):
-        return self.base + 32 * i if self.have[i] else None
+def _call(name: str, dev: int, stream, *args):
+    """One C call on the stream (None: dev's current one), with dev current: a launch on
+    another device's stream fails."""
+    f = getattr(_lib or lib(), name)
+    if torch._C._cuda_getDevice() == dev:
+        st = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if st != MQ_OK:
+        _check(st, name)
 
 
 class Weight:
@@ -427,7 +414,7 @@ class Weight:
 
     def __init__(self, base: dict, packed: dict | None = None):
         self.N, self.K = base["rows"], base["cols"]
-        self.base, self.packed = base, packed
+        self.base, self.packed, self.dev = base, packed, base["codes"].get_device()
         self._mat, self._res = mat(base), packed_struct(packed)
         self.base_ptr = ctypes.addressof(self._mat)
         self.packed_ptr = None if self._res is None else ctypes.addressof(self._res)
@@ -442,10 +429,10 @@ class KVCache:
             raise MosaicError("pages: a contiguous uint8 tensor [pages][heads][page_size / 16][18 D], D = 64 or 128")
         self.pages, self.k_scale, self.v_scale = pages, k_scale, v_scale
         self.num_pages, self.heads, self.D = pages.shape[0], pages.shape[1], pages.shape[3] // 18
-        self.page_size = 16 * pages.shape[2]
+        self.page_size, self.dev = 16 * pages.shape[2], pages.get_device()
         for s in (k_scale, v_scale):
             if s is not None:
-                _index(s, torch.float32, self.heads, pages, "tensor scales")
+                _index(s, torch.float32, self.heads, pages.get_device(), "tensor scales")
         self._struct = KVCacheStruct(_ptr(pages), self.num_pages, self.page_size, self.heads, self.D, _ptr(k_scale),
                                      _ptr(v_scale))
         self.ptr = ctypes.addressof(self._struct)
@@ -460,27 +447,20 @@ class KVCache:
 
 def mq_gemv(X: torch.Tensor, w: Weight, Y: torch.Tensor, flags: int = 0, stream=None):
     """Y [M][N] = X [M][K] times the packed weight, X in 16 bits (not quantized), M <= 16."""
-    ty = _type(X, Y)
+    ty, dev = _kind(X), X.get_device()
     (M, K), (My, N) = X.shape, Y.shape
-    if K != w.K or N != w.N or My != M or X.stride(1) != 1 or Y.stride(1) != 1:
-        raise MosaicError(f"mq_gemv: X [M][{w.K}] and Y [M][{w.N}] are wanted, got {tuple(X.shape)} and {tuple(Y.shape)}")
-    with _on(X, stream) as s:
-        st = lib().mq_gemv(X.data_ptr(), ty, X.stride(0), w.base_ptr, w.packed_ptr, Y.data_ptr(), Y.stride(0), M, N, K,
-                           flags, s)
-    _check(st, "mq_gemv")
+    (xs, x1), (ys, y1) = X.stride(), Y.stride()
+    if K != w.K or N != w.N or My != M or x1 != 1 or y1 != 1 or Y.dtype != X.dtype or Y.get_device() != dev or w.dev != dev:
+        raise MosaicError(f"mq_gemv: X [M][{w.K}] and Y [M][{w.N}] of one 16-bit type on cuda:{w.dev} are wanted, got "
+                          f"{tuple(X.shape)} {X.dtype} on {X.device} and {tuple(Y.shape)} {Y.dtype} on {Y.device}")
+    _call("mq_gemv", dev, stream, X.data_ptr(), ty, xs, w.base_ptr, w.packed_ptr, Y.data_ptr(), ys, M, N, K, flags)
 
 
-def _turn(T, pos, freq, like):
+def _turn(T, pos, freq, dev):
     """(pos pointer, freq pointer, rot) of a rotation; freq None: no rotation."""
     if freq is None:
         return None, None, 0
-    return _index(pos, torch.int64, T, like, "pos"), _index(freq, torch.float64, 1, like, "freq"), 2 * freq.numel()
-
-
-def _norm_weight(w, D, like):
-    if w is None:
-        return None
-    return _index(w, like.dtype, D, like, "norm weight")
+    return _index(pos, torch.int64, T, dev, "pos"), _index(freq, torch.float64, 1, dev, "freq"), 2 * freq.numel()
 
 
 def mq_qk_norm_rope(q, k, q_out, k_out, pos=None, freq=None, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -488,54 +468,48 @@ def mq_qk_norm_rope(q, k, q_out, k_out, pos=None, freq=None, q_weight=None, k_we
     """Head norms and the rotation of q [T][heads][D] and k (either may be None); the
     outputs may be the inputs. freq: fp64 [rot / 2] radians a position."""
     x = q if q is not None else k
-    ty = _type(x, q, k, q_out, k_out)
+    ty, dt, dev = _kind(x), x.dtype, x.get_device()
     T, _, D = x.shape
-    h = _heads(T, D, q, k, q_out, k_out)
-    pp, fp, rot = _turn(T, pos, freq, x)
-    with _on(x, stream) as s:
-        st = lib().mq_qk_norm_rope(h.at(0), h.at(1), h.at(2), h.at(3), T, D, ty, _norm_weight(q_weight, D, x),
-                                   _norm_weight(k_weight, D, x), eps, pp, fp, rot, interleaved, s)
-    _check(st, "mq_qk_norm_rope")
+    pp, fp, rot = _turn(T, pos, freq, dev)
+    _call("mq_qk_norm_rope", dev, stream, _put(0, q, T, D, dt, dev), _put(1, k, T, D, dt, dev),
+          _put(2, q_out, T, D, dt, dev), _put(3, k_out, T, D, dt, dev), T, D, ty,
+          None if q_weight is None else _index(q_weight, dt, D, dev, "q_weight"),
+          None if k_weight is None else _index(k_weight, dt, D, dev, "k_weight"), eps, pp, fp, rot, interleaved)
 
 
 def mq_kv_append(k, v, slots, cache: KVCache, stream=None):
     """Rows k, v [T][heads][D] into the cache at slots (int64 [T], negative: skipped)."""
-    ty = _type(k, v)
+    ty, dt, dev, D = _kind(k), k.dtype, cache.dev, cache.D
     T = k.shape[0]
-    h = _heads(T, cache.D, k, v)
-    with _on(cache.pages, stream) as s:
-        st = lib().mq_kv_append(h.at(0), h.at(1), T, ty, _index(slots, torch.int64, T, k, "slots"), cache.ptr, s)
-    _check(st, "mq_kv_append")
+    _call("mq_kv_append", dev, stream, _put(0, k, T, D, dt, dev), _put(1, v, T, D, dt, dev), T, ty,
+          _index(slots, torch.int64, T, dev, "slots"), cache.ptr)
 
 
 def mq_qkv_append(q, k, v, q_out, slots, cache: KVCache, pos=None, freq=None, q_weight=None, k_weight=None,
                   eps: float = 1e-6, interleaved: bool = False, k_out=None, stream=None):
     """mq_qk_norm_rope and mq_kv_append in one launch (the turned keys go to the cache, and
     to k_out if given)."""
-    ty = _type(q, k, v, q_out, k_out)
+    ty, dt, dev, D = _kind(q), q.dtype, cache.dev, cache.D
     T = q.shape[0]
-    h = _heads(T, cache.D, q, k, v, q_out, k_out)
-    pp, fp, rot = _turn(T, pos, freq, q)
-    with _on(cache.pages, stream) as s:
-        st = lib().mq_qkv_append(h.at(0), h.at(1), h.at(2), h.at(3), h.at(4), T, ty, _norm_weight(q_weight, cache.D, q),
-                                 _norm_weight(k_weight, cache.D, q), eps, pp, fp, rot, interleaved,
-                                 _index(slots, torch.int64, T, q, "slots"), cache.ptr, s)
-    _check(st, "mq_qkv_append")
+    pp, fp, rot = _turn(T, pos, freq, dev)
+    _call("mq_qkv_append", dev, stream, _put(0, q, T, D, dt, dev), _put(1, k, T, D, dt, dev), _put(2, v, T, D, dt, dev),
+          _put(3, q_out, T, D, dt, dev), _put(4, k_out, T, D, dt, dev), T, ty,
+          None if q_weight is None else _index(q_weight, dt, D, dev, "q_weight"),
+          None if k_weight is None else _index(k_weight, dt, D, dev, "k_weight"), eps, pp, fp, rot, interleaved,
+          _index(slots, torch.int64, T, dev, "slots"), cache.ptr)
 
 
 def mq_kv_read(cache: KVCache, slots, k, v, stream=None):
     """The cached rows of slots (int64 [T]) as 16-bit k, v [T][heads][D]."""
-    ty = _type(k, v)
+    ty, dt, dev, D = _kind(k), k.dtype, cache.dev, cache.D
     T = k.shape[0]
-    h = _heads(T, cache.D, k, v)
-    with _on(cache.pages, stream) as s:
-        st = lib().mq_kv_read(cache.ptr, _index(slots, torch.int64, T, k, "slots"), T, h.at(0), h.at(1), ty, s)
-    _check(st, "mq_kv_read")
+    _call("mq_kv_read", dev, stream, cache.ptr, _index(slots, torch.int64, T, dev, "slots"), T,
+          _put(0, k, T, D, dt, dev), _put(1, v, T, D, dt, dev), ty)
 
 
 def kv_attention_workspace(q: torch.Tensor, cache: KVCache, max_q: int = 1) -> torch.Tensor | None:
     """Zeroed workspace for mq_kv_attention with q's heads (see include/mosaic_ops.h)."""
-    with _on(q):
+    with torch.cuda.device(q.device):
         n = lib().mq_kv_attention_workspace_bytes(q.shape[1], cache.heads, cache.D, max_q)
     return torch.zeros(n, dtype=torch.uint8, device=q.device) if n else None
 
@@ -545,22 +519,19 @@ def mq_kv_attention(q, cache: KVCache, block_table, kv_len, out, scale: float, c
     """out [T][heads][D] = attention of q over the cached tokens. block_table: int32 [B][pages],
     kv_len: int32 [B], cu_q: int32 [B + 1] or None (one query token a sequence), lse: fp32
     [T][heads] or None, ws: kv_attention_workspace(q, cache, max_q)."""
-    ty = _type(q, out)
+    ty, dt, dev, D = _kind(q), q.dtype, cache.dev, cache.D
     T, B = q.shape[0], kv_len.shape[0]
-    h = _heads(T, cache.D, q, out)
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.device != q.device or \
-            block_table.shape[0] < B or block_table.stride(1) != 1:
-        raise MosaicError("block_table: int32 [B][pages] on q's device")
-    if lse is not None:
-        _index(lse, torch.float32, T * q.shape[1], q, "lse")
-    with _on(cache.pages, stream) as s:
-        st = lib().mq_kv_attention(
-            h.at(0), h.at(1), None if lse is None else lse.data_ptr(), T, ty, cache.ptr, block_table.data_ptr(),
-            block_table.stride(0), block_table.shape[1], B,
-            None if cu_q is None else _index(cu_q, torch.int32, B + 1, q, "cu_q"), max_q,
-            _index(kv_len, torch.int32, B, q, "kv_len"), scale, window, None if ws is None else ws.data_ptr(),
-            0 if ws is None else ws.numel(), s)
-    _check(st, "mq_kv_attention")
+    tb, pages = block_table.shape
+    ts, t1 = block_table.stride()
+    if block_table.dtype != torch.int32 or block_table.get_device() != dev or tb < B or t1 != 1:
+        raise MosaicError(f"block_table: int32 [{B}][pages] on cuda:{dev} is wanted")
+    if ws is not None and ws.get_device() != dev:
+        raise MosaicError(f"the workspace must lie on cuda:{dev}")
+    _call("mq_kv_attention", dev, stream, _put(0, q, T, D, dt, dev), _put(1, out, T, D, dt, dev),
+          None if lse is None else _index(lse, torch.float32, T * q.shape[1], dev, "lse"), T, ty, cache.ptr,
+          block_table.data_ptr(), ts, pages, B, None if cu_q is None else _index(cu_q, torch.int32, B + 1, dev, "cu_q"),
+          max_q, _index(kv_len, torch.int32, B, dev, "kv_len"), scale, window, None if ws is None else ws.data_ptr(),
+          0 if ws is None else ws.numel())
 
 
 # ------------------------------------------------------------------ convenience
