@@ -1,10 +1,13 @@
-"""Build libmosaic.so (CUDA, sm_100a) in-tree with nvcc."""
+"""Build libmosaic.so (CUDA, sm_100a) in-tree with nvcc, and _marshal.so (the operators' operand
+checks, C++ against PyTorch's headers) with g++."""
 from __future__ import annotations
 
 import glob
 import os
+import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -14,6 +17,9 @@ LIB = os.path.join(PKG, "libmosaic.so")
 # the same library with MQ_TIMELINE defined: the small decode GEMM records per-CTA event
 # times (mq_timeline_read); used by timeline.py, never by the path
 LIB_TIMELINE = os.path.join(PKG, "libmosaic_timeline.so")
+
+MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -44,6 +50,7 @@ def stale(lib: str = LIB) -> bool:
 
 def build(force: bool = False, verbose: bool = False, timeline: bool = False) -> str:
     lib = LIB_TIMELINE if timeline else LIB
+    build_marshal()
     if not (force or stale(lib)):
         return lib
     nvcc = os.environ.get("NVCC", "nvcc")
@@ -55,6 +62,26 @@ def build(force: bool = False, verbose: bool = False, timeline: bool = False) ->
     return lib
 
 
+def build_marshal(force: bool = False) -> str:
+    """The Python extension, built for the running interpreter and its PyTorch."""
+    newest = max(os.path.getmtime(p) for p in [MARSHAL_SRC, __file__, *glob.glob(os.path.join(INCLUDE, "*.h"))])
+    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= newest:
+        return MARSHAL
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(os.environ.get("NVCC", "nvcc")) or "/usr/local/cuda/bin/nvcc")))
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    subprocess.check_call([
+        os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + INCLUDE,
+        "-isystem", os.path.join(base, "include"), "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+        "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"], "-o", tmp, MARSHAL_SRC,
+        "-L" + os.path.join(base, "lib"), "-Wl,-rpath," + os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_python"])
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 if __name__ == "__main__":
+    build_marshal(force=True)
     build(force=True, verbose="-v" in sys.argv)
     print(LIB)

@@ -1,4 +1,6 @@
-"""ctypes binding of libmosaic (include/mosaic.h).
+"""Binding of libmosaic: ctypes for include/mosaic.h, and a small extension module for the
+operators of include/mosaic_ops.h (csrc/marshal.cpp: their calls are short enough for the
+host's side of a call to show).
 
 Argument marshalling only: every step of the path runs in the CUDA library. PyTorch
 provides device memory and the current stream. There is no CPU fallback: a missing
@@ -7,10 +9,7 @@ library or a non-CUDA tensor raises.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
-import struct
-import threading
 
 import torch
 
@@ -349,63 +348,26 @@ def gemm_workspace(M: int, N: int, K: int, flags: int, device) -> torch.Tensor |
 
 
 # ------------------------------------------------------------------ mosaic_ops.h
-_TYPES = {torch.bfloat16: MQ_BF16, torch.float16: MQ_F16}
+_marshal = None
 
 
-class _Scratch(threading.local):
-    """Five mq_heads that a call fills and the C side has read when the call returns."""
-
-    def __init__(self):
-        self.buf = (ctypes.c_int64 * 20)()
-        self.at = [ctypes.addressof(self.buf) + 32 * i for i in range(5)]
-        self.put = [functools.partial(struct.Struct("4q").pack_into, self.buf, 32 * i) for i in range(5)]
-
-
-_scratch = _Scratch()
-
-
-def _kind(t: torch.Tensor) -> int:
-    """The mq_dtype of a 16-bit CUDA tensor."""
-    code = _TYPES.get(t.dtype)
-    if code is None:
-        raise MosaicError(f"bf16 or fp16 tensors are taken, not {t.dtype}")
-    if not t.is_cuda:
-        raise MosaicError("libmosaic takes CUDA tensors only")
-    return code
+def _ops():
+    """The extension module that checks these operators' operands and calls the library (csrc/marshal.cpp)."""
+    global _marshal
+    if _marshal is None:
+        L = lib()
+        if not os.path.exists(os.path.join(_PKG, "_marshal.so")):
+            raise MosaicError("_marshal.so is not built; run __graft_entry__.build()")
+        from . import _marshal as m
+        m.bind(MosaicError, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
+            "mq_gemv", "mq_qk_norm_rope", "mq_kv_append", "mq_qkv_append", "mq_kv_read", "mq_kv_attention",
+            "mq_status_string")))
+        _marshal = m
+    return _marshal
 
 
-def _put(i: int, t, T: int, D: int, dtype, dev: int):
-    """Address of mq_heads i, filled from t [T][heads][D] (None: None)."""
-    if t is None:
-        return None
-    n, h, d = t.shape
-    st, sh, sd = t.stride()
-    if n != T or d != D or sd != 1 or t.dtype != dtype or t.get_device() != dev:
-        raise MosaicError(f"[{T}][heads][{D}] of {dtype} on cuda:{dev} with adjacent elements is wanted, got shape "
-                          f"{tuple(t.shape)}, strides {t.stride()}, {t.dtype} on {t.device}")
-    _scratch.put[i](t.data_ptr(), h, st, sh)
-    return _scratch.at[i]
-
-
-def _index(t: torch.Tensor, dtype, numel: int, dev: int, what: str) -> int:
-    """Pointer of a contiguous array of at least numel elements on cuda:dev."""
-    if t.dtype != dtype or t.get_device() != dev or t.numel() < numel or not t.is_contiguous():
-        raise MosaicError(f"{what}: {numel} contiguous {dtype} values on cuda:{dev} are wanted, got {t.dtype} "
-                          f"{tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _call(name: str, dev: int, stream, *args):
-    """One C call on the stream (None: dev's current one), with dev current: a launch on
-    another device's stream fails."""
-    f = getattr(_lib or lib(), name)
-    if torch._C._cuda_getDevice() == dev:
-        st = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
-    else:
-        with torch.cuda.device(dev):
-            st = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
-    if st != MQ_OK:
-        _check(st, name)
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 class Weight:
@@ -432,7 +394,8 @@ class KVCache:
         self.page_size, self.dev = 16 * pages.shape[2], pages.get_device()
         for s in (k_scale, v_scale):
             if s is not None:
-                _index(s, torch.float32, self.heads, pages.get_device(), "tensor scales")
+                if s.dtype != torch.float32 or s.device != pages.device or s.numel() < self.heads or not s.is_contiguous():
+                    raise MosaicError(f"tensor scales: {self.heads} contiguous fp32 values on {pages.device} are wanted")
         self._struct = KVCacheStruct(_ptr(pages), self.num_pages, self.page_size, self.heads, self.D, _ptr(k_scale),
                                      _ptr(v_scale))
         self.ptr = ctypes.addressof(self._struct)
@@ -447,64 +410,32 @@ class KVCache:
 
 def mq_gemv(X: torch.Tensor, w: Weight, Y: torch.Tensor, flags: int = 0, stream=None):
     """Y [M][N] = X [M][K] times the packed weight, X in 16 bits (not quantized), M <= 16."""
-    ty, dev = _kind(X), X.get_device()
-    (M, K), (My, N) = X.shape, Y.shape
-    (xs, x1), (ys, y1) = X.stride(), Y.stride()
-    if K != w.K or N != w.N or My != M or x1 != 1 or y1 != 1 or Y.dtype != X.dtype or Y.get_device() != dev or w.dev != dev:
-        raise MosaicError(f"mq_gemv: X [M][{w.K}] and Y [M][{w.N}] of one 16-bit type on cuda:{w.dev} are wanted, got "
-                          f"{tuple(X.shape)} {X.dtype} on {X.device} and {tuple(Y.shape)} {Y.dtype} on {Y.device}")
-    _call("mq_gemv", dev, stream, X.data_ptr(), ty, xs, w.base_ptr, w.packed_ptr, Y.data_ptr(), ys, M, N, K, flags)
-
-
-def _turn(T, pos, freq, dev):
-    """(pos pointer, freq pointer, rot) of a rotation; freq None: no rotation."""
-    if freq is None:
-        return None, None, 0
-    return _index(pos, torch.int64, T, dev, "pos"), _index(freq, torch.float64, 1, dev, "freq"), 2 * freq.numel()
+    (_marshal or _ops()).gemv(X, Y, w.N, w.K, w.dev, w.base_ptr, w.packed_ptr, flags, _raw(stream))
 
 
 def mq_qk_norm_rope(q, k, q_out, k_out, pos=None, freq=None, q_weight=None, k_weight=None, eps: float = 1e-6,
                     interleaved: bool = False, stream=None):
     """Head norms and the rotation of q [T][heads][D] and k (either may be None); the
     outputs may be the inputs. freq: fp64 [rot / 2] radians a position."""
-    x = q if q is not None else k
-    ty, dt, dev = _kind(x), x.dtype, x.get_device()
-    T, _, D = x.shape
-    pp, fp, rot = _turn(T, pos, freq, dev)
-    _call("mq_qk_norm_rope", dev, stream, _put(0, q, T, D, dt, dev), _put(1, k, T, D, dt, dev),
-          _put(2, q_out, T, D, dt, dev), _put(3, k_out, T, D, dt, dev), T, D, ty,
-          None if q_weight is None else _index(q_weight, dt, D, dev, "q_weight"),
-          None if k_weight is None else _index(k_weight, dt, D, dev, "k_weight"), eps, pp, fp, rot, interleaved)
+    (_marshal or _ops()).qk_norm_rope(q, k, q_out, k_out, pos, freq, q_weight, k_weight, eps, interleaved, _raw(stream))
 
 
 def mq_kv_append(k, v, slots, cache: KVCache, stream=None):
     """Rows k, v [T][heads][D] into the cache at slots (int64 [T], negative: skipped)."""
-    ty, dt, dev, D = _kind(k), k.dtype, cache.dev, cache.D
-    T = k.shape[0]
-    _call("mq_kv_append", dev, stream, _put(0, k, T, D, dt, dev), _put(1, v, T, D, dt, dev), T, ty,
-          _index(slots, torch.int64, T, dev, "slots"), cache.ptr)
+    (_marshal or _ops()).kv_append(k, v, slots, cache.ptr, cache.dev, _raw(stream))
 
 
 def mq_qkv_append(q, k, v, q_out, slots, cache: KVCache, pos=None, freq=None, q_weight=None, k_weight=None,
                   eps: float = 1e-6, interleaved: bool = False, k_out=None, stream=None):
     """mq_qk_norm_rope and mq_kv_append in one launch (the turned keys go to the cache, and
     to k_out if given)."""
-    ty, dt, dev, D = _kind(q), q.dtype, cache.dev, cache.D
-    T = q.shape[0]
-    pp, fp, rot = _turn(T, pos, freq, dev)
-    _call("mq_qkv_append", dev, stream, _put(0, q, T, D, dt, dev), _put(1, k, T, D, dt, dev), _put(2, v, T, D, dt, dev),
-          _put(3, q_out, T, D, dt, dev), _put(4, k_out, T, D, dt, dev), T, ty,
-          None if q_weight is None else _index(q_weight, dt, D, dev, "q_weight"),
-          None if k_weight is None else _index(k_weight, dt, D, dev, "k_weight"), eps, pp, fp, rot, interleaved,
-          _index(slots, torch.int64, T, dev, "slots"), cache.ptr)
+    (_marshal or _ops()).qkv_append(q, k, v, q_out, k_out, pos, freq, q_weight, k_weight, eps, interleaved, slots,
+                                    cache.ptr, cache.dev, _raw(stream))
 
 
 def mq_kv_read(cache: KVCache, slots, k, v, stream=None):
     """The cached rows of slots (int64 [T]) as 16-bit k, v [T][heads][D]."""
-    ty, dt, dev, D = _kind(k), k.dtype, cache.dev, cache.D
-    T = k.shape[0]
-    _call("mq_kv_read", dev, stream, cache.ptr, _index(slots, torch.int64, T, dev, "slots"), T,
-          _put(0, k, T, D, dt, dev), _put(1, v, T, D, dt, dev), ty)
+    (_marshal or _ops()).kv_read(cache.ptr, cache.dev, slots, k, v, _raw(stream))
 
 
 def kv_attention_workspace(q: torch.Tensor, cache: KVCache, max_q: int = 1) -> torch.Tensor | None:
@@ -519,19 +450,8 @@ def mq_kv_attention(q, cache: KVCache, block_table, kv_len, out, scale: float, c
     """out [T][heads][D] = attention of q over the cached tokens. block_table: int32 [B][pages],
     kv_len: int32 [B], cu_q: int32 [B + 1] or None (one query token a sequence), lse: fp32
     [T][heads] or None, ws: kv_attention_workspace(q, cache, max_q)."""
-    ty, dt, dev, D = _kind(q), q.dtype, cache.dev, cache.D
-    T, B = q.shape[0], kv_len.shape[0]
-    tb, pages = block_table.shape
-    ts, t1 = block_table.stride()
-    if block_table.dtype != torch.int32 or block_table.get_device() != dev or tb < B or t1 != 1:
-        raise MosaicError(f"block_table: int32 [{B}][pages] on cuda:{dev} is wanted")
-    if ws is not None and ws.get_device() != dev:
-        raise MosaicError(f"the workspace must lie on cuda:{dev}")
-    _call("mq_kv_attention", dev, stream, _put(0, q, T, D, dt, dev), _put(1, out, T, D, dt, dev),
-          None if lse is None else _index(lse, torch.float32, T * q.shape[1], dev, "lse"), T, ty, cache.ptr,
-          block_table.data_ptr(), ts, pages, B, None if cu_q is None else _index(cu_q, torch.int32, B + 1, dev, "cu_q"),
-          max_q, _index(kv_len, torch.int32, B, dev, "kv_len"), scale, window, None if ws is None else ws.data_ptr(),
-          0 if ws is None else ws.numel())
+    (_marshal or _ops()).kv_attention(q, cache.ptr, cache.dev, block_table, kv_len, out, scale, cu_q, max_q, window, lse, ws,
+                                      _raw(stream))
 
 
 # ------------------------------------------------------------------ convenience
