@@ -142,15 +142,15 @@ namespace mq {
 // For the operators of ops.cu.
 mq_status count_launches(cudaError_t e, int kernels) { return launched(e, kernels); }
 int* device_error_word() { return err_word(); }
-bool tensor_map_rows64(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows) {
+bool tensor_map_w64(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[2] = {row_bytes, rows};
     cuuint64_t strides[1] = {row_bytes};
-    cuuint32_t box[2] = {64, 64};
+    cuuint32_t box[2] = {128, 64};
     cuuint32_t es[2] = {1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -3,19 +3,20 @@
 //
 // What bounds it: the weight's bytes (9/16 a weight, 2304 a residual block), read once.
 //
-// The work of 64 weight rows is a list of steps: 128 columns of the base each, then two
+// The work of 64 weight rows is a list of steps: 256 columns of the base each, then four
 // residual blocks each (a block row's blocks lie one behind the other). In both a lane of
-// a warp takes 32 adjacent columns of its rows, at a column of its own, which a product's
+// a warp takes 64 adjacent columns of its rows, at a column of its own, which a product's
 // free order of k allows; so a residual step is as dense as a base step. A step's codes
-// (4 KB: one TMA box of 64 bytes x 64 rows, or two packed blocks by one bulk copy) and scales (1 KB, one
-// bulk copy) go to the warp's own ring in shared memory. Steps are this short so that 16
-// warps fit an SM: with twice the columns and half the warps the waits of a step show
-// (28672 x 8192, one token: 45.1 us against TODO).
+// (8 KB, one TMA box, 128-byte swizzle; or four packed blocks, one bulk copy) and scales
+// (2 KB, one bulk copy) go to the warp's own ring in shared memory.
 //
 // The weights are the 16-row operand of fp16 tensor-core products (val * dec(sf) is exact
-// in fp16), eight tokens the other one. bf16 activations are scaled by a power of two per
-// token and step to fit fp16 (what falls below is under 2^-39 of the step's largest), and the
-// step's fp32 sums scaled back.
+// in fp16), eight tokens the other one. A first kernel writes the activations as that operand: in
+// fp16, bf16 ones scaled by a power of two per token (the largest element to [2^14, 2^15); what falls
+// below is under 2^-39 of it), in the order in which lanes read them. Formed inside the products'
+// kernel instead, by every CTA again, they cost it a fifth to a half of its time (16 tokens through
+// 14336 x 4096: 28.3 us against TODO). The two kernels overlap: the weight's copies do not wait for
+// the first one.
 //
 // The steps of a row tile are dealt to the warps of a cluster of S CTAs, S so that the CTAs
 // about fill the GPU; the warps' sums are added in their order through shared memory, then
@@ -33,34 +34,91 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 2;
 constexpr int kRows = 64;              // weight rows of a tile (a block row)
-constexpr int kCols = 128;             // base columns of a step
+constexpr int kCols = 256;             // base columns of a step
 constexpr int kCodes = kRows * kCols / 2;
-constexpr int kStage = kCodes + 1024;  // codes, then two 512-byte scale chunks
+constexpr int kStage = kCodes + 2048;  // codes, then four 512-byte scale chunks
+constexpr int kCtasPerSm = 2;
+constexpr int kXThreads = 512, kXKeep = 4;  // of the operand's kernel: 16384 columns are read once
 constexpr int kPitch = kRows + 4;      // floats of a token's row in the sums
 
-template <int NT>
-constexpr int ctas_per_sm() { return NT == 1 ? 4 : 3; }
+constexpr size_t smem_bytes() { return (size_t)kWarps * (kStages * kStage + kStages * 8); }
 
-template <int NT>
-constexpr size_t smem_bytes() { return (size_t)kWarps * (kStages * kStage + NT * 2048 + kStages * 8); }
+// Bytes of the operand: per 64-column chunk and eight tokens 1 KB, [piece of 8 columns][token], and
+// every token's scale.
+size_t operand_bytes(int nt, int K) { return (size_t)(K / 64) * nt * 1024 + 8 * nt * sizeof(float); }
+
+// A CTA a token (those past M: zeros).
+template <bool F16>
+__global__ void __launch_bounds__(kXThreads) k_gemv_x(const uint16_t* __restrict__ X, int64_t ldx, int M, int NT, int K,
+                                                      uint8_t* __restrict__ out, float* __restrict__ back) {
+    __shared__ uint32_t tops[kXThreads / 32];
+    const int m = blockIdx.x, pieces = K / 8;
+    griddep_wait();
+    griddep_launch();
+    const uint4* src = reinterpret_cast<const uint4*>(X + m * ldx);
+    uint4 keep[kXKeep];  // the first pieces, read once
+#pragma unroll
+    for (int i = 0; i < kXKeep; ++i) {
+        const int c = threadIdx.x + i * kXThreads;
+        keep[i] = m < M && c < pieces ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+    }
+    uint32_t ex = 15u;
+    if constexpr (!F16) {
+        // the largest element's bits, two at a time
+        auto top_of = [](const uint4& w) {
+            return __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu), __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+        };
+        uint32_t a = 0;
+#pragma unroll
+        for (int i = 0; i < kXKeep; ++i) a = __vmaxu2(a, top_of(keep[i]));
+        if (m < M)
+            for (int c = threadIdx.x + kXKeep * kXThreads; c < pieces; c += kXThreads) a = __vmaxu2(a, top_of(__ldg(src + c)));
+        const uint32_t top = __reduce_max_sync(0xffffffffu, max(a & 0xFFFFu, a >> 16));
+        if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+        __syncthreads();
+        for (int i = 0; i < kXThreads / 32; ++i) ex = max(ex, tops[i] >> 7);
+    }
+    const float up = __uint_as_float((268u - ex) << 23);
+    auto put = [&](int c, const uint4& v) {
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if constexpr (!F16) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float2 f = widen2<false>(w[q]);
+                w[q] = narrow2<true>(f.x * up, f.y * up);
+            }
+        }
+        *reinterpret_cast<uint4*>(out + (((int64_t)(c >> 3) * NT + (m >> 3)) * 8 + (c & 7)) * 128 + (m & 7) * 16) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+    };
+#pragma unroll
+    for (int i = 0; i < kXKeep; ++i) {
+        const int c = threadIdx.x + i * kXThreads;
+        if (c < pieces) put(c, keep[i]);
+    }
+    for (int c = threadIdx.x + kXKeep * kXThreads; c < pieces; c += kXThreads)
+        put(c, m < M ? __ldg(src + c) : make_uint4(0, 0, 0, 0));
+    if (threadIdx.x == 0) back[m] = F16 ? 1.0f : __uint_as_float((ex - 14u) << 23);
+}
 
 template <int NT, bool F16>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_gemv(const __grid_constant__ CUtensorMap tw, const GemvParams p) {
-    extern __shared__ __align__(128) uint8_t smem[];
-    uint64_t(*full)[kStages] = reinterpret_cast<uint64_t(*)[kStages]>(smem + kWarps * (kStages * kStage + NT * 2048));
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) k_gemv(const __grid_constant__ CUtensorMap tw, const GemvParams p) {
+    // The swizzle's pattern repeats every 1024 bytes. Without static shared memory the array
+    // starts on such a boundary (checked below), and two CTAs fit an SM.
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint64_t(*full)[kStages] = reinterpret_cast<uint64_t(*)[kStages]>(smem + kWarps * kStages * kStage);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int tile = blockIdx.y, S = gridDim.x, rank = blockIdx.x, KC = p.K / 64;
     if (tid < kWarps * kStages) mbar_init(&full[0][0] + tid, 1);
     mbar_fence_init();
     if (tid == 0) tma_prefetch_desc(&tw);
     __syncthreads();
-    if (!p.w_ready) {
-        griddep_wait();
-        griddep_launch();
+    if (smem_u32(smem) & 1023u) {
+        if (tid == 0) report_index(p.err);
+        return;
     }
-    const int nbase = p.base ? (KC + 1) / 2 : 0, step0 = rank * kWarps + warp, stride = S * kWarps;
+    const int nbase = p.base ? (KC + 3) / 4 : 0, step0 = rank * kWarps + warp, stride = S * kWarps;
     uint8_t* ring = smem + warp * (kStages * kStage);
-    uint8_t* frag = smem + kWarps * kStages * kStage + warp * (NT * 2048);  // this warp's activations as fp16 operands
     int res0 = 0, res1 = 0;
 
     auto issue = [&](int i) {
@@ -69,55 +127,52 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_gemv(const __gr
             uint8_t* dst = ring + (i % kStages) * kStage;
             uint64_t* bar = &full[warp][i % kStages];
             if (step < nbase) {
-                const uint32_t sf = (uint32_t)min(2, KC - 2 * step) * 512;
+                const uint32_t sf = (uint32_t)min(4, KC - 4 * step) * 512;
                 mbar_arrive_expect_tx(bar, kCodes + sf);
                 tma_load_2d(dst, &tw, bar, step * (kCols / 2), tile * kRows);
-                bulk_load(dst + kCodes, p.sf + ((int64_t)(tile >> 1) * KC + 2 * step) * 512, sf, bar);
+                bulk_load(dst + kCodes, p.sf + ((int64_t)(tile >> 1) * KC + 4 * step) * 512, sf, bar);
             } else {
-                const int e = res0 + 2 * (step - nbase);
-                const uint32_t n = (uint32_t)min(2, res1 - e);
+                const int e = res0 + 4 * (step - nbase);
+                const uint32_t n = (uint32_t)min(4, res1 - e);
                 mbar_arrive_expect_tx(bar, n * 2560);
                 bulk_load(dst, p.blk_codes + (int64_t)e * 2048, n * 2048, bar);
                 bulk_load(dst + kCodes, p.blk_sf + (int64_t)e * 512, n * 512, bar);
             }
         }
     };
-    // the first base steps fly before the residual's extent is known
+    // The operand's kernel lets this one start after its own wait: all that came before it, the
+    // weight's writers among them, has ended. The first base steps fly before the residual's
+    // extent is known.
     int ahead = 0;
     while (ahead < kStages && step0 + ahead * stride < nbase) issue(ahead++);
     if (p.blk_codes) {
         res0 = __ldg(p.tile_ptr + tile);
         res1 = __ldg(p.tile_ptr + tile + 1);
     }
-    const int total = nbase + (res1 - res0 + 1) / 2;
+    const int total = nbase + (res1 - res0 + 3) / 4;
     const int steps = step0 < total ? (total - step0 + stride - 1) / stride : 0;
     while (ahead < min(kStages, steps)) issue(ahead++);
-    // Column chunk c (0 or 1, 64 columns) of a step, -1 past the end.
+    // Column chunk c (0..3, 64 columns) of a step, -1 past the end.
     auto chunk_of = [&](int i, int c) {
         const int step = step0 + i * stride;
-        if (step < nbase) return 2 * step + c < KC ? 2 * step + c : -1;
-        const int e = res0 + 2 * (step - nbase) + c;
+        if (step < nbase) return 4 * step + c < KC ? 4 * step + c : -1;
+        const int e = res0 + 4 * (step - nbase) + c;
         return e < res1 ? __ldg(p.blk_kt + e) : -1;
     };
-    const int half = lane >> 4, piece = lane & 15;  // of a pair of tokens, and of a token's 128 activations
-    int kt = steps > 0 ? chunk_of(0, piece >> 3) : -1;
-    // tokens past M are zeros, and stay
-    for (int i = lane; i < NT * 128; i += 32) reinterpret_cast<uint4*>(frag)[i] = make_uint4(0, 0, 0, 0);
-    if (p.w_ready) {
-        griddep_wait();
-        griddep_launch();
-    }
+    int kt = steps > 0 ? chunk_of(0, t) : -1, ktn = steps > 1 ? chunk_of(1, t) : -1;
+    griddep_wait();
+    griddep_launch();
 
-    uint4 xr[4 * NT];  // eight activations of tokens 2 i + half
-    auto load_x = [&](int kt) {
-        const uint16_t* src = p.X + 64 * (int64_t)kt + 8 * (piece & 7) + half * p.ldx;
+    uint4 b[NT][4];  // the lane's operand in 32 of its 64 columns, half a step ahead
+    auto load_x = [&](int kt, int h) {
+        const uint8_t* src = p.xop + (int64_t)kt * (NT * 1024) + (4 * h) * 128 + g * 16;
 #pragma unroll
-        for (int i = 0; i < 4 * NT; ++i)
-            if (2 * i < p.M)
-                xr[i] = kt >= 0 && 2 * i + half < p.M ? __ldg(reinterpret_cast<const uint4*>(src + 2 * i * p.ldx))
-                                                      : make_uint4(0, 0, 0, 0);
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                b[nt][w] = kt >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + nt * 1024 + w * 128)) : make_uint4(0, 0, 0, 0);
     };
-    load_x(kt);
+    load_x(kt, 0);
 
     float acc[4][NT][4];
 #pragma unroll
@@ -130,109 +185,62 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_gemv(const __gr
     bool alive = true;
     for (int i = 0; i < steps; ++i) {
         const int step = step0 + i * stride;
-        // columns of this lane's rows
-        const bool valid = step < nbase ? 2 * step + (t >> 1) < KC : res0 + 2 * (step - nbase) + (t >> 1) < res1;
-        // Activations to fp16, as operands: piece j (two products) of lane l's columns at slot
-        // l ^ 2j, so that neither these stores nor the loads below meet in a bank.
-        float back[NT][2] = {};  // scale of this lane's result columns, tokens 8 nt + 2t, + 1
-#pragma unroll
-        for (int m = 0; m < 4 * NT; ++m) {
-            if (2 * m >= p.M) continue;
-            uint32_t w[4] = {xr[m].x, xr[m].y, xr[m].z, xr[m].w};
-            if constexpr (!F16) {
-                // the largest element's bits (bf16, two at a time), over a token's 16 lanes
-                uint32_t a = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
-                                      __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
-                uint32_t top = max(a & 0xFFFFu, a >> 16);
-#pragma unroll
-                for (int x = 1; x < 16; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
-                // the largest element to [2^14, 2^15)
-                const uint32_t ex = max(top >> 7, 15u);
-                const float up = __uint_as_float((268u - ex) << 23);
-                const float d = __uint_as_float((ex - 14u) << 23);
-                const float d0 = __shfl_sync(0xffffffffu, d, 0), d1 = __shfl_sync(0xffffffffu, d, 16);
-                if ((m & 3) == t) {
-                    back[m / 4][0] = d0;
-                    back[m / 4][1] = d1;
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float2 f = widen2<false>(w[q]);
-                    w[q] = narrow2<true>(f.x * up, f.y * up);
-                }
-            }
-            // token 2m + half; its piece 4 t' + j
-            const int j = piece & 3, slot = (4 * (2 * (m & 3) + half) + (piece >> 2)) ^ (2 * j);
-            *reinterpret_cast<uint4*>(frag + (m / 4) * 2048 + j * 512 + slot * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        __syncwarp();
-        kt = i + 1 < steps ? chunk_of(i + 1, piece >> 3) : -1;
-        load_x(kt);
-
+        const bool valid = step < nbase ? 4 * step + t < KC : res0 + 4 * (step - nbase) + t < res1;  // columns of this lane's rows
         const uint32_t parity = (i / kStages) & 1u;
         // the warp decides together; after a wait that gave up (reported) nothing is issued or waited for
         if (__any_sync(0xffffffffu, !mbar_try_wait(&full[warp][i % kStages], parity)) && alive)
             alive = __all_sync(0xffffffffu, mbar_wait_err(&full[warp][i % kStages], parity, p.err));
         const uint8_t* buf = ring + (i % kStages) * kStage;
-        // Scales of rows 16 rt + 8 hf + g in the lane's 32 columns (two groups): a 128-row chunk
-        // holds row r's four at (r % 32) * 16 + (r / 32) * 4. Columns past the end may hold
-        // anything: zero.
-        uint32_t sc[4][2];
+        // scales of rows 16 rt + 8 hf + g in the lane's 64 columns: a 128-row chunk holds row
+        // r's four at (r % 32) * 16 + (r / 32) * 4. Columns past the end may hold anything: zero.
+        uint32_t sc[4][2][2];
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                const uint2 w = *reinterpret_cast<const uint2*>(buf + kCodes + (t >> 1) * 512 + (16 * q + 8 * hf + g) * 16 + (tile & 1) * 8);
-                const uint32_t both = __byte_perm(w.x, w.y, (t & 1) ? 0x7632 : 0x5410);
-                e4m3x4_half(valid ? both : 0u, sc[q][hf], sc[q + 2][hf]);
+                uint2 w = *reinterpret_cast<const uint2*>(buf + kCodes + t * 512 + (16 * q + 8 * hf + g) * 16 + (tile & 1) * 8);
+                if (!valid) w = make_uint2(0, 0);
+                e4m3x4_half(w.x, sc[q][hf][0], sc[q][hf][1]);
+                e4m3x4_half(w.y, sc[q + 2][hf][0], sc[q + 2][hf][1]);
             }
-        float cc[4][NT][4];
-        // 16 bytes of row g: rows of 64 bytes, or packed blocks (lane pair = half a block)
+        // 16-byte piece h of the lane's columns in row r: swizzled rows of 128 bytes, or packed blocks
         const bool isb = step < nbase;
-        const uint8_t* codes = isb ? buf + g * 64 + t * 16 : buf + (t >> 1) * 2048 + (t & 1) * 128 + g * 16;
-        const int row8 = isb ? 512 : 256;  // eight rows further
-        uint4 b[NT][4];
+        const uint8_t* codes = isb ? buf + g * 128 : buf + t * 2048 + g * 16;
+        const int row8 = isb ? 1024 : 256;  // eight rows further
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            const uint8_t* at = codes + (isb ? ((2 * t + h) ^ g) * 16 : h * 128);
+            uint4 x0[NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int w = 0; w < 4; ++w) b[nt][w] = *reinterpret_cast<const uint4*>(frag + nt * 2048 + w * 512 + (lane ^ (2 * w)) * 16);
+                for (int w = 0; w < 4; ++w) x0[nt][w] = b[nt][w];
+            load_x(h ? ktn : kt, h ^ 1);
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-            const uint4 a0 = *reinterpret_cast<const uint4*>(codes + (2 * rt) * row8);
-            const uint4 a1 = *reinterpret_cast<const uint4*>(codes + (2 * rt + 1) * row8);
-            const uint32_t w0[4] = {a0.x, a0.y, a0.z, a0.w}, w1[4] = {a1.x, a1.y, a1.z, a1.w};
+            for (int rt = 0; rt < 4; ++rt) {
+                const uint4 a0 = *reinterpret_cast<const uint4*>(at + (2 * rt) * row8);
+                const uint4 a1 = *reinterpret_cast<const uint4*>(at + (2 * rt + 1) * row8);
+                const uint32_t s0 = h ? sc[rt][0][1] : sc[rt][0][0], s1 = h ? sc[rt][1][1] : sc[rt][1][0];
+                const uint32_t w0[4] = {a0.x, a0.y, a0.z, a0.w}, w1[4] = {a1.x, a1.y, a1.z, a1.w};
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                uint32_t x[4], y[4];
-                e2m1x8_half(w0[w], x);
-                e2m1x8_half(w1[w], y);
-                const __half2 f0 = w < 2 ? low2(sc[rt][0]) : high2(sc[rt][0]), f1 = w < 2 ? low2(sc[rt][1]) : high2(sc[rt][1]);
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t x[4], y[4];
+                    e2m1x8_half(w0[w], x);
+                    e2m1x8_half(w1[w], y);
+                    const __half2 f0 = w < 2 ? low2(s0) : high2(s0), f1 = w < 2 ? low2(s1) : high2(s1);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t a[4] = {mul_h2(x[2 * e], f0), mul_h2(y[2 * e], f1), mul_h2(x[2 * e + 1], f0),
-                                           mul_h2(y[2 * e + 1], f1)};
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t a[4] = {mul_h2(x[2 * e], f0), mul_h2(y[2 * e], f1), mul_h2(x[2 * e + 1], f0),
+                                               mul_h2(y[2 * e + 1], f1)};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const uint32_t b0 = e ? b[nt][w].z : b[nt][w].x, b1 = e ? b[nt][w].w : b[nt][w].y;
-                        if constexpr (F16) {
-                            mma_f16(acc[rt][nt], a, b0, b1);
-                        } else {
-                            if (w == 0 && e == 0)
-                                mma_f16_first(cc[rt][nt], a, b0, b1);
-                            else
-                                mma_f16(cc[rt][nt], a, b0, b1);
-                        }
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_f16(acc[rt][nt], a, e ? x0[nt][w].z : x0[nt][w].x, e ? x0[nt][w].w : x0[nt][w].y);
                     }
                 }
             }
         }
-        if constexpr (!F16)
-#pragma unroll
-            for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[rt][nt][c] = __fmaf_rn(cc[rt][nt][c], back[nt][c & 1], acc[rt][nt][c]);
+        kt = ktn;
+        ktn = i + 2 < steps ? chunk_of(i + 2, t) : -1;
         __syncwarp();
         if (i + kStages < steps && alive) issue(i + kStages);
     }
@@ -252,6 +260,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_gemv(const __gr
                 sums[(warp * 8 * NT + 8 * nt + 2 * t + (c & 1)) * kPitch + 16 * rt + g + 8 * (c >> 1)] = acc[rt][nt][c];
     __syncthreads();
     const float gw = __ldg(p.g_w);
+    const float* back = reinterpret_cast<const float*>(p.xop + (int64_t)KC * (NT * 1024));  // the tokens' scales
     float* mine = sums + kWarps * 8 * NT * kPitch;  // [token][kPitch], this CTA's
     for (int i = tid; i < kRows * p.M; i += kThreads) {
         const int m = i / kRows, n = i % kRows;
@@ -259,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_gemv(const __gr
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) v += sums[(w * 8 * NT + m) * kPitch + n];
         if (S == 1)
-            p.Y[m * p.ldy + tile * kRows + n] = (uint16_t)narrow2<F16>(v * gw, 0.0f);
+            p.Y[m * p.ldy + tile * kRows + n] = (uint16_t)narrow2<F16>(v * __ldg(back + m) * gw, 0.0f);
         else
             mine[m * kPitch + n] = v;
     }
@@ -269,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_gemv(const __gr
             const int m = i / kRows, n = i % kRows;
             float v = 0.0f;
             for (int r = 0; r < S; ++r) v += ld_dsmem_f32(mine + m * kPitch + n, r);
-            p.Y[m * p.ldy + tile * kRows + n] = (uint16_t)narrow2<F16>(v * gw, 0.0f);
+            p.Y[m * p.ldy + tile * kRows + n] = (uint16_t)narrow2<F16>(v * __ldg(back + m) * gw, 0.0f);
         }
         cluster_sync();  // no CTA leaves while another reads its sums
     }
@@ -278,19 +287,25 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_gemv(const __gr
 template <int NT, bool F16>
 cudaError_t gemv_of(const CUtensorMap& tw, const GemvParams& p, int S, cudaStream_t s) {
     static std::atomic<bool> done[64];
-    const cudaError_t e = once_per_device(done, [] {
-        return cudaFuncSetAttribute(k_gemv<NT, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<NT>());
+    cudaError_t e = once_per_device(done, [] {
+        return cudaFuncSetAttribute(k_gemv<NT, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes());
     });
     if (e != cudaSuccess) return e;
-    return launch_pdl_cluster(k_gemv<NT, F16>, dim3(S, p.N / kRows), dim3(kThreads), smem_bytes<NT>(), s, dim3(S, 1, 1), tw, p);
+    uint8_t* xop = p.xop;
+    e = launch_pdl(k_gemv_x<F16>, dim3(8 * NT), dim3(kXThreads), 0, s, 1, p.X, p.ldx, p.M, NT, p.K, xop,
+                   reinterpret_cast<float*>(xop + (int64_t)(p.K / 64) * (NT * 1024)));
+    if (e != cudaSuccess) return e;
+    return launch_pdl_cluster(k_gemv<NT, F16>, dim3(S, p.N / kRows), dim3(kThreads), smem_bytes(), s, dim3(S, 1, 1), tw, p);
 }
 
 }  // namespace
 
+size_t gemv_workspace(int M, int K) { return operand_bytes(M <= 8 ? 1 : 2, K); }
+
 cudaError_t launch_gemv(const CUtensorMap& tw, const GemvParams& p, bool f16, cudaStream_t s) {
-    const int tiles = p.N / kRows, steps = (p.K / 64 + 1) / 2;
+    const int tiles = p.N / kRows, steps = (p.K / 64 + 3) / 4;
     // CTAs that fill the GPU once, none without a step for each of its warps
-    const int S = std::max(1, std::min({8, (p.M <= 8 ? ctas_per_sm<1>() : ctas_per_sm<2>()) * device_sms() / tiles, steps / kWarps}));
+    const int S = std::max(1, std::min({8, kCtasPerSm * device_sms() / tiles, steps / kWarps}));
     if (p.M <= 8) return f16 ? gemv_of<1, true>(tw, p, S, s) : gemv_of<1, false>(tw, p, S, s);
     return f16 ? gemv_of<2, true>(tw, p, S, s) : gemv_of<2, false>(tw, p, S, s);
 }

@@ -7,7 +7,9 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -27,6 +29,7 @@ struct Lib {
     decltype(&mq_kv_read) kv_read;
     decltype(&mq_kv_attention) kv_attention;
     decltype(&mq_status_string) status_string;
+    decltype(&mq_gemv_workspace_bytes) gemv_workspace_bytes;
 } lib;
 PyObject* mosaic_error = nullptr;
 
@@ -150,9 +153,9 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F&& f) {
     return nullptr;
 }
 
-// (X, Y, N, K, device, weight, residual, flags, stream)
+// (X, Y, N, K, device, weight, residual, flags, stream, workspace)
 PyObject* py_gemv(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 9, [&] {
+    return guarded(n, 10, [&] {
         const at::Tensor &X = tensor(a[0], "X"), &Y = tensor(a[1], "Y");
         const Common c(X);
         const int64_t N = integer(a[2]), K = integer(a[3]), dev = integer(a[4]);
@@ -161,8 +164,20 @@ PyObject* py_gemv(PyObject*, PyObject* const* a, Py_ssize_t n) {
             throw Refused("X [M][" + std::to_string(K) + "] and Y [M][" + std::to_string(N) + "] of one 16-bit type on cuda:" +
                           std::to_string(dev) + " are wanted, got X " + shape_of(X) + ", Y " + shape_of(Y));
         OnDevice d(c.dev, a[8]);
+        // no workspace given: one from the caching allocator, which hands it on in the stream's order
+        at::Tensor ws;
+        const size_t need = lib.gemv_workspace_bytes(extent(X.size(0)), (int)K);
+        if (a[9] != Py_None) {
+            array<void>(a[9], "ws", at::kByte, 0, c.dev);
+            ws = tensor(a[9], "ws");
+        } else if (need > 0) {
+            c10::cuda::OptionalCUDAStreamGuard g;
+            if (a[8] != Py_None) g.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(d.stream), c.dev));
+            ws = at::empty({(int64_t)need}, X.options().dtype(at::kByte));
+        }
         return done(lib.gemv(X.data_ptr(), c.code, X.stride(0), pointer<mq_nvfp4_mat>(a[5]), pointer<mq_residual_packed>(a[6]),
-                             Y.data_ptr(), Y.stride(0), extent(X.size(0)), (int)N, (int)K, (unsigned)integer(a[7]), d.stream),
+                             Y.data_ptr(), Y.stride(0), extent(X.size(0)), (int)N, (int)K, (unsigned)integer(a[7]),
+                             ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? (size_t)ws.numel() : 0, d.stream),
                     "mq_gemv");
     });
 }
@@ -273,14 +288,14 @@ PyObject* py_kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// (error class, addresses of the seven functions in Lib's order)
+// (error class, addresses of the eight functions in Lib's order)
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (n != 8) {
-        PyErr_SetString(PyExc_TypeError, "bind: an error class and seven addresses");
+    if (n != 9) {
+        PyErr_SetString(PyExc_TypeError, "bind: an error class and eight addresses");
         return nullptr;
     }
-    void* at[7];
-    for (int i = 0; i < 7; ++i) {
+    void* at[8];
+    for (int i = 0; i < 8; ++i) {
         at[i] = PyLong_AsVoidPtr(a[i + 1]);
         if (!at[i]) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind: a null address");
@@ -297,6 +312,7 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     lib.kv_read = reinterpret_cast<decltype(lib.kv_read)>(at[4]);
     lib.kv_attention = reinterpret_cast<decltype(lib.kv_attention)>(at[5]);
     lib.status_string = reinterpret_cast<decltype(lib.status_string)>(at[6]);
+    lib.gemv_workspace_bytes = reinterpret_cast<decltype(lib.gemv_workspace_bytes)>(at[7]);
     Py_RETURN_NONE;
 }
 

@@ -52,8 +52,13 @@ size_t mq_kv_cache_bytes(int num_pages, int page_size, int heads, int D) {
     return (size_t)num_pages * (size_t)heads * (size_t)(page_size / 16) * (size_t)(18 * D);
 }
 
+size_t mq_gemv_workspace_bytes(int M, int K) {
+    if (M <= 0 || M > 16 || K <= 0 || K % 64) return 0;
+    return gemv_workspace(M, K);
+}
+
 mq_status mq_gemv(const void* X, mq_dtype type, int64_t ldx, const mq_nvfp4_mat* wq, const mq_residual_packed* r,
-                  void* Y, int64_t ldy, int M, int N, int K, unsigned flags, mq_stream stream) {
+                  void* Y, int64_t ldy, int M, int N, int K, unsigned flags, void* ws, size_t ws_bytes, mq_stream stream) {
     if (!X || !wq || !Y || !type_ok(type) || M <= 0 || N <= 0 || K <= 0 || N % 64 || K % 64) return MQ_ERR_INVALID_ARG;
     if (flags & ~(unsigned)(MQ_GEMM_BASE_ONLY | MQ_GEMM_RESIDUAL_ONLY | MQ_GEMM_WEIGHTS_READY)) return MQ_ERR_INVALID_ARG;
     if ((flags & MQ_GEMM_BASE_ONLY) && (flags & MQ_GEMM_RESIDUAL_ONLY)) return MQ_ERR_INVALID_ARG;
@@ -65,6 +70,7 @@ mq_status mq_gemv(const void* X, mq_dtype type, int64_t ldx, const mq_nvfp4_mat*
         if (!aligned(r->blk_codes, 16) || !aligned(r->blk_sf, 16)) return MQ_ERR_INVALID_ARG;
     }
     if (M > 16) return MQ_ERR_UNSUPPORTED_SHAPE;
+    if (!ws || ws_bytes < mq_gemv_workspace_bytes(M, K) || !aligned(ws, 16)) return MQ_ERR_WORKSPACE;
     const bool has_r = r && r->nblk > 0 && !(flags & MQ_GEMM_BASE_ONLY);
     GemvParams p;
     memset(&p, 0, sizeof p);
@@ -85,11 +91,11 @@ mq_status mq_gemv(const void* X, mq_dtype type, int64_t ldx, const mq_nvfp4_mat*
     p.N = N;
     p.K = K;
     p.base = (flags & MQ_GEMM_RESIDUAL_ONLY) ? 0 : 1;
-    p.w_ready = (flags & MQ_GEMM_WEIGHTS_READY) ? 1 : 0;
+    p.xop = static_cast<uint8_t*>(ws);
     p.err = device_error_word();
     CUtensorMap tw;
-    if (!p.err || !tensor_map_rows64(&tw, wq->codes, (uint64_t)K / 2, (uint64_t)N)) return MQ_ERR_CUDA;
-    return count_launches(launch_gemv(tw, p, type == MQ_F16, as_stream(stream)), 1);
+    if (!p.err || !tensor_map_w64(&tw, wq->codes, (uint64_t)K / 2, (uint64_t)N)) return MQ_ERR_CUDA;
+    return count_launches(launch_gemv(tw, p, type == MQ_F16, as_stream(stream)), 2);
 }
 
 // q, k, v, q_out, k_out, slots and cache as the entry points say; absent ones are null.

@@ -102,7 +102,7 @@ struct GemvParams {
     int64_t ldy;
     int M, N, K;
     int base;     // 0: the residual alone
-    int w_ready;  // the weight was complete before this kernel could start
+    uint8_t* xop;  // workspace: the activations as an operand
     int* err;
 };
 
@@ -127,13 +127,14 @@ struct AttnParams {
 // api.cu: a launch's status, counted in mq_launch_count; the current device's error word
 mq_status count_launches(cudaError_t e, int kernels);
 int* device_error_word();
-// a byte matrix in boxes of 64 bytes x 64 rows, not swizzled; zeros outside
-bool tensor_map_rows64(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows);
+// a byte matrix in boxes of 128 bytes x 64 rows, 128-byte swizzle; zeros outside
+bool tensor_map_w64(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows);
 int device_sms();  // gemm.cu: SMs of the current device (148 without one)
 
 cudaError_t launch_heads(const HeadsParams& p, int D, bool f16, cudaStream_t s);
 cudaError_t launch_kv_read(const HeadsParams& p, int D, bool f16, cudaStream_t s);
-// tw: the codes (tensor_map_rows64)
+// tw: the codes (tensor_map_w64)
+size_t gemv_workspace(int M, int K);
 cudaError_t launch_gemv(const CUtensorMap& tw, const GemvParams& p, bool f16, cudaStream_t s);
 // bytes: partials, then counters at *counters_at
 size_t attn_workspace(int q_heads, int kv_heads, int D, int max_q, size_t* counters_at);

@@ -33,7 +33,7 @@ EXPORTED = (
     "mq_gemm_noalloc", "mq_gemm_noalloc_scratch_limit", "mq_quantize_weight_delta", "mq_topk_blocks",
     "mq_pack_residual_weight", "mq_gemm_act", "mq_weight_bytes", "mq_fp4_mma_loop", "mq_fp4_mma_loop_flops",
     "mq_test_arm_wait_fault", "mq_smooth_scales", "mq_smooth_apply", "mq_timeline_read",
-    "mq_kv_cache_bytes", "mq_gemv", "mq_qk_norm_rope", "mq_kv_append", "mq_qkv_append", "mq_kv_read",
+    "mq_kv_cache_bytes", "mq_gemv", "mq_gemv_workspace_bytes", "mq_qk_norm_rope", "mq_kv_append", "mq_qkv_append", "mq_kv_read",
     "mq_kv_attention_workspace_bytes", "mq_kv_attention",
 )
 
@@ -138,7 +138,9 @@ def lib():
     L.mq_kv_cache_bytes.restype = sz
     L.mq_kv_attention_workspace_bytes.argtypes = [i32] * 4
     L.mq_kv_attention_workspace_bytes.restype = sz
-    L.mq_gemv.argtypes = [vp, i32, i64, vp, vp, vp, i64, i32, i32, i32, u32, vp]
+    L.mq_gemv.argtypes = [vp, i32, i64, vp, vp, vp, i64, i32, i32, i32, u32, vp, sz, vp]
+    L.mq_gemv_workspace_bytes.argtypes = [i32, i32]
+    L.mq_gemv_workspace_bytes.restype = sz
     L.mq_qk_norm_rope.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp, f32, vp, vp, i32, i32, vp]
     L.mq_kv_append.argtypes = [vp, vp, i32, i32, vp, vp, vp]
     L.mq_qkv_append.argtypes = [vp, vp, vp, vp, vp, i32, i32, vp, vp, f32, vp, vp, i32, i32, vp, vp, vp]
@@ -361,7 +363,7 @@ def _ops():
         from . import _marshal as m
         m.bind(MosaicError, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
             "mq_gemv", "mq_qk_norm_rope", "mq_kv_append", "mq_qkv_append", "mq_kv_read", "mq_kv_attention",
-            "mq_status_string")))
+            "mq_status_string", "mq_gemv_workspace_bytes")))
         _marshal = m
     return _marshal
 
@@ -408,9 +410,10 @@ class KVCache:
                    v_scale)
 
 
-def mq_gemv(X: torch.Tensor, w: Weight, Y: torch.Tensor, flags: int = 0, stream=None):
-    """Y [M][N] = X [M][K] times the packed weight, X in 16 bits (not quantized), M <= 16."""
-    (_marshal or _ops()).gemv(X, Y, w.N, w.K, w.dev, w.base_ptr, w.packed_ptr, flags, _raw(stream))
+def mq_gemv(X: torch.Tensor, w: Weight, Y: torch.Tensor, flags: int = 0, stream=None, ws=None):
+    """Y [M][N] = X [M][K] times the packed weight, X in 16 bits (not quantized), M <= 16. ws:
+    mq_gemv_workspace_bytes(M, K) bytes, or None: a block of PyTorch's caching allocator."""
+    (_marshal or _ops()).gemv(X, Y, w.N, w.K, w.dev, w.base_ptr, w.packed_ptr, flags, _raw(stream), ws)
 
 
 def mq_qk_norm_rope(q, k, q_out, k_out, pos=None, freq=None, q_weight=None, k_weight=None, eps: float = 1e-6,

@@ -74,11 +74,16 @@ size_t mq_kv_cache_bytes(int num_pages, int page_size, int heads, int D);
  * m * ldx elements (16-byte aligned, ldx % 8 == 0); Y: [M][N], row m at m * ldy.
  * 1 <= M <= 16 tokens (MQ_ERR_UNSUPPORTED_SHAPE above: mq_gemm serves those), any N and K
  * that are multiples of 64. wq: codes, sf_swz (both 16-byte aligned), gscale [1]. r as in
- * mq_gemm, with blk_kt. flags: 0 or MQ_GEMM_BASE_ONLY / MQ_GEMM_RESIDUAL_ONLY /
- * MQ_GEMM_WEIGHTS_READY (as there). Repeated calls give the same bits. No workspace.
+ * mq_gemm, with blk_kt. flags: 0 or MQ_GEMM_BASE_ONLY / MQ_GEMM_RESIDUAL_ONLY;
+ * MQ_GEMM_WEIGHTS_READY is taken and changes nothing (the weight is read while the activations
+ * are prepared in any case). Repeated calls give the same bits. ws: mq_gemv_workspace_bytes,
+ * 16-byte aligned, any contents; calls that share one must not overlap on the GPU.
  */
 mq_status mq_gemv(const void* X, mq_dtype type, int64_t ldx, const mq_nvfp4_mat* wq, const mq_residual_packed* r,
-                  void* Y, int64_t ldy, int M, int N, int K, unsigned flags, mq_stream stream);
+                  void* Y, int64_t ldy, int M, int N, int K, unsigned flags, void* ws, size_t ws_bytes, mq_stream stream);
+
+/* The activations as a tensor-core operand. 0 on a bad shape. */
+size_t mq_gemv_workspace_bytes(int M, int K);
 
 /*
  * RMS norm of every query and key head and the position rotation, in one pass:

@@ -60,8 +60,13 @@ def test_gemv_refusals(L, buf):
     r = mosaic.ResidualPacked(N, K, 2, buf(4096), buf(1024), buf(8), buf(12), buf(8))
     X, Y = buf(17 * K * 2), buf(17 * N * 2)
 
-    def call(X=X, ty=0, ldx=K, w=w, r=None, Y=Y, ldy=N, M=M, N=N, K=K, flags=0):
-        return L.mq_gemv(X, ty, ldx, ctypes.byref(w) if w else None, ctypes.byref(r) if r else None, Y, ldy, M, N, K, flags, None)
+    n = L.mq_gemv_workspace_bytes(M, K)
+    ws = buf(n)
+    assert n > 0 and L.mq_gemv_workspace_bytes(17, K) == 0 and L.mq_gemv_workspace_bytes(0, K) == 0
+    assert L.mq_gemv_workspace_bytes(1, 96) == 0
+
+    def call(X=X, ty=0, ldx=K, w=w, r=None, Y=Y, ldy=N, M=M, N=N, K=K, flags=0, ws=ws, n=n):
+        return L.mq_gemv(X, ty, ldx, ctypes.byref(w) if w else None, ctypes.byref(r) if r else None, Y, ldy, M, N, K, flags, ws, n, None)
 
     assert call(X=None) == 1 and call(Y=None) == 1 and call(w=None) == 1 and call(ty=2) == 1
     assert call(M=0) == 1 and call(N=96) == 1 and call(K=96) == 1 and call(N=192) == 1
@@ -69,6 +74,7 @@ def test_gemv_refusals(L, buf):
     assert call(X=X + 8) == 1 and call(Y=Y + 1) == 1
     assert call(flags=2) == 1 and call(flags=4 | 8) == 1 and call(flags=16) == 1
     assert call(M=17) == 2
+    assert call(ws=None) == 3 and call(n=n - 1) == 3 and call(ws=ws + 8) == 3
     assert call(r=mosaic.ResidualPacked(N, K, 2, buf(4096), buf(1024), None, buf(12), None)) == 1
     assert call(r=mosaic.ResidualPacked(N, 2 * K, 2, *[getattr(r, f) for f in ("blk_codes", "blk_sf", "blk_kt", "tile_ptr", "bitmap")])) == 1
     assert call(w=mosaic.NVFP4Mat(N, K, w.codes, None, None, w.gscale)) == 1
