@@ -40,6 +40,7 @@ constexpr int kStep = 32;               // tokens a warp takes at a time
 constexpr int kUnit = kStep * kWarps;   // tokens of a unit
 constexpr int kStages = 2;              // steps in flight per warp (a power of two)
 constexpr int kJoin = 4;                // what a second run costs a CTA, in units
+constexpr int kMaxLen = 1 << 30;        // cached tokens of a sequence
 constexpr float kShift = 7.0f;          // exponent offset of the fp16 softmax weights
 constexpr float kSlack = 8.0f;          // how far a score may pass its row's reference
 
@@ -74,7 +75,7 @@ __device__ __forceinline__ Seq seq_of(const AttnParams& p, int b, bool report) {
         if (report) report_index(p.err);
         s.row0 = s.nq = 0;
     }
-    if (s.len < 0 || s.len > (int64_t)p.max_pages * p.cache.page_size) {
+    if (s.len < 0 || s.len > kMaxLen || s.len > (int64_t)p.max_pages * p.cache.page_size) {
         if (report) report_index(p.err);
         s.len = 0;
     }
@@ -807,10 +808,12 @@ int grid_of(int nt) { return device_sms() * (nt == 1 ? ctas_per_sm<1>() : ctas_p
 
 }  // namespace
 
-size_t attn_workspace(int q_heads, int kv_heads, int D, int max_q, size_t* counters_at) {
-    const int nt = row_tiles(q_heads, kv_heads, max_q), grid = grid_of(nt);
-    *counters_at = (size_t)2 * grid * slot_floats(nt, D) * sizeof(float);
-    return *counters_at + (size_t)grid * sizeof(int);
+// Counters first, in the same place for every shape: the partial sums of one must not fall on
+// the counters of another that shares the workspace.
+size_t attn_workspace(int q_heads, int kv_heads, int D, int max_q, size_t* partials_at) {
+    const int nt = row_tiles(q_heads, kv_heads, max_q);
+    *partials_at = ((size_t)device_sms() * ctas_per_sm<1>() * sizeof(int) + 255) / 256 * 256;
+    return *partials_at + (size_t)2 * grid_of(nt) * slot_floats(nt, D) * sizeof(float);
 }
 
 cudaError_t launch_attn(const AttnParams& p0, int D, int max_q, bool f16, cudaStream_t s) {

@@ -15,7 +15,7 @@
 // fp16, bf16 ones scaled by a power of two per token (the largest element to [2^14, 2^15); what falls
 // below is under 2^-39 of it), in the order in which lanes read them. Formed inside the products'
 // kernel instead, by every CTA again, they cost it a fifth to a half of its time (16 tokens through
-// 14336 x 4096: 28.3 us against TODO). The two kernels overlap: the weight's copies do not wait for
+// 14336 x 4096: 28.3 us against 18.3; one through 28672 x 8192: 45.1 against 43.4). The two kernels overlap: the weight's copies do not wait for
 // the first one.
 //
 // The steps of a row tile are dealt to the warps of a cluster of S CTAs, S so that the CTAs

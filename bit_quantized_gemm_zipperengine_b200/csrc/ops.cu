@@ -196,9 +196,10 @@ mq_status mq_kv_attention(const mq_heads* q, const mq_heads* out, float* lse, in
     if (q->heads % cache->heads || !block_table || !kv_len || max_pages <= 0 || (B > 1 && table_stride < max_pages))
         return MQ_ERR_INVALID_ARG;
     if (!cu_q && T != B) return MQ_ERR_INVALID_ARG;
-    size_t counters_at;
-    const size_t need = attn_workspace((int)q->heads, cache->heads, D, max_q, &counters_at);
-    if (need > 0 && (!ws || ws_bytes < need || !aligned(ws, 16))) return MQ_ERR_WORKSPACE;
+    if ((int64_t)T * (q->heads / cache->heads) > (1 << 30)) return MQ_ERR_UNSUPPORTED_SHAPE;  // rows are counted in 32 bits
+    size_t partials_at;
+    const size_t need = attn_workspace((int)q->heads, cache->heads, D, max_q, &partials_at);
+    if (!ws || ws_bytes < need || !aligned(ws, 16)) return MQ_ERR_WORKSPACE;
     AttnParams p;
     memset(&p, 0, sizeof p);
     p.q = view(q);
@@ -214,8 +215,8 @@ mq_status mq_kv_attention(const mq_heads* q, const mq_heads* out, float* lse, in
     p.kv_len = kv_len;
     p.scale = scale;
     p.window = window;
-    p.partial = static_cast<float*>(ws);
-    p.counters = need > 0 ? reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + counters_at) : nullptr;
+    p.counters = static_cast<int*>(ws);
+    p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + partials_at);
     p.err = device_error_word();
     if (!p.err) return MQ_ERR_CUDA;
     return count_launches(launch_attn(p, D, max_q, type == MQ_F16, as_stream(stream)), 1);

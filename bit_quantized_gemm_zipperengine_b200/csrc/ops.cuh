@@ -136,8 +136,8 @@ cudaError_t launch_kv_read(const HeadsParams& p, int D, bool f16, cudaStream_t s
 // tw: the codes (tensor_map_w64)
 size_t gemv_workspace(int M, int K);
 cudaError_t launch_gemv(const CUtensorMap& tw, const GemvParams& p, bool f16, cudaStream_t s);
-// bytes: partials, then counters at *counters_at
-size_t attn_workspace(int q_heads, int kv_heads, int D, int max_q, size_t* counters_at);
+// bytes: counters, then partial sums at *partials_at
+size_t attn_workspace(int q_heads, int kv_heads, int D, int max_q, size_t* partials_at);
 cudaError_t launch_attn(const AttnParams& p, int D, int max_q, bool f16, cudaStream_t s);
 
 }  // namespace mq

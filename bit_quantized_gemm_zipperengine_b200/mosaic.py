@@ -588,6 +588,8 @@ class AttentionLayer:
             with torch.cuda.stream(stream):
                 return self.step(X, pos, slots, block_table, kv_len, cu_q, max_q)
         T, D, H, Hq = X.shape[0], self.cache.D, self.cache.heads, self.q_heads
+        if T == 0:
+            return X.new_empty((0, self.out.N))
         y = self._project(self.qkv, X).view(T, Hq + 2 * H, D)
         q, k, v = y[:, :Hq], y[:, Hq:Hq + H], y[:, Hq + H:]
         mq_qkv_append(q, k, v, q, slots, self.cache, pos, self.freq, self.q_norm, self.k_norm, self.eps,

@@ -90,7 +90,8 @@ size_t mq_gemv_workspace_bytes(int M, int K);
  *   u = x * (mean_d x^2 + eps)^(-1/2) * w_d      (q_weight / k_weight NULL: u = x)
  *   (a, b) -> (a cos - b sin, b cos + a sin), angle = pos[t] * freq[i],
  * over the pairs (u_i, u_{i + rot/2}), or (u_2i, u_{2i+1}) if interleaved, i < rot / 2;
- * elements from rot on are not turned. fp32 arithmetic, rounded once; the angle is formed
+ * elements from rot on are not turned. eps >= 0 (with 0, a row of zeros has no norm: NaN). fp32
+ * arithmetic, rounded once; the angle is formed
  * and reduced in fp64. q, k: [T][heads][D]; q_out, k_out of the same heads (may be the
  * input itself, not a shifted view of it). pos: [T] (any value within +-2^53), freq: fp64 [rot/2] radians
  * a position. D = 64, 128 or 256, rot a multiple of 16 from 0 to D (0: pos and freq may be
@@ -127,10 +128,12 @@ mq_status mq_qkv_append(const mq_heads* q, const mq_heads* k, const mq_heads* v,
 mq_status mq_kv_read(const mq_kv_cache* cache, const int64_t* slots, int T, const mq_heads* k, const mq_heads* v,
                      mq_dtype type, mq_stream stream);
 
-/* Workspace of mq_kv_attention for the current device: partial results of the pieces into
- * which it cuts long sequences, and their counters. The counters must be zero before the
- * first call on a workspace; every call leaves them zero. Calls that share a workspace must
- * not overlap on the GPU (two captured graphs included). 0 on a bad shape. */
+/* Workspace of mq_kv_attention for the current device: counters, then partial results of the
+ * pieces into which it cuts long sequences. All zero before the first call on a workspace;
+ * every call leaves the counters zero (one that ended in MQ_ERR_TIMEOUT may not: zero it
+ * again), so calls of any shapes may take turns on one that is large enough for each. Calls
+ * that share a workspace must not overlap on the GPU (two captured graphs included). 0 on a
+ * bad shape. */
 size_t mq_kv_attention_workspace_bytes(int q_heads, int kv_heads, int D, int max_q);
 
 /*
@@ -143,8 +146,8 @@ size_t mq_kv_attention_workspace_bytes(int q_heads, int kv_heads, int D, int max
  * Query head h reads cache head h / (q heads / cache heads). A row that sees nothing gets
  * zeros (lse -inf). Scores, softmax sums and outputs are held in fp32; the softmax weights
  * enter the second product in fp16. Rows of q that belong to no sequence leave out and lse
- * as they were. A page outside the cache, a length past the table or a row past T is left
- * out and reported. q, out: [T][q heads][D] (distinct); lse: fp32 [T][q heads] or NULL.
+ * as they were. A page outside the cache, a length past the table (or 2^30) or a row past T is
+ * left out and reported. q, out: [T][q heads][D] (distinct); lse: fp32 [T][q heads] or NULL.
  * max_q: the largest number of query tokens of a sequence that the caller expects (it
  * picks the kernel and sizes ws; more are served too). q heads a multiple of cache heads.
  * Repeated calls give the same bits. T >= 0, B >= 0.

@@ -105,6 +105,42 @@ def test_gemv_far_magnitudes(big, dev, mosaic):
     within(y, want, gemv_bound(x, W, want, 2.0 ** -20, BF, K))
 
 
+def test_gemv_graphs_streams_and_workspaces(dev, mosaic):
+    """A captured call replayed with other activations, calls on two streams at once, and a
+    workspace of the caller's that an earlier call left full."""
+    N, K, M = 512, 1024, 3
+    base, packed = ref.random_weight(N, K, 20, 5, dev)
+    w = mosaic.Weight(base, packed)
+    W, g = ref.dense_weight(base, packed), float(base["gscale"])
+    gen = torch.Generator().manual_seed(4)
+    x, y = torch.randn(M, K, generator=gen).to(BF).to(dev), torch.empty(M, N, dtype=BF, device=dev)
+    mosaic.mq_gemv(x, w, y)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mosaic.mq_gemv(x, w, y)
+    for scale in (1.0, 1e-20, 300.0):
+        x.copy_((scale * torch.randn(M, K, generator=gen)).to(BF))
+        graph.replay()
+        want = x.double() @ W.t() * g
+        within(y, want, gemv_bound(x, W, want, g, BF, K))
+    xs = [torch.randn(m, K, generator=gen).to(BF).to(dev) for m in (1, 16)]
+    ys = [torch.empty(t.shape[0], N, dtype=BF, device=dev) for t in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for t, o, s in zip(xs, ys, streams):
+            mosaic.mq_gemv(t, w, o, stream=s)
+    torch.cuda.synchronize()
+    ws = torch.full((mosaic.lib().mq_gemv_workspace_bytes(16, K),), 0x7F, dtype=torch.uint8, device=dev)
+    for t, o in zip(xs, ys):
+        want = t.double() @ W.t() * g
+        within(o, want, gemv_bound(t, W, want, g, BF, K))
+        again = torch.empty_like(o)
+        mosaic.mq_gemv(t, w, again, ws=ws)
+        assert torch.equal(o, again)
+
+
 def test_gemv_on_a_prepared_layer(dev, mosaic):
     """The buffers that the layer's own preparation wrote, next to mq_gemm on the same weight."""
     L = synth.layer("tiny")
@@ -315,6 +351,9 @@ CASES = [
     ([1030] + [9] * 40, [1] * 41, 8, 2, 128, 16, 0),  # one long among many short
     ([5000], [1], 8, 1, 128, 64, 0),                  # cut into many pieces
     ([3001, 2999], [3, 4], 16, 2, 64, 16, 0),
+    ([97, 500, 48, 49], [1] * 4, 8, 4, 128, 48, 0),   # pages that are no power of two
+    ([(7 * i) % 90 for i in range(300)], [1] * 300, 8, 2, 64, 16, 0),             # more sequences than threads of a CTA
+    ([40 + (11 * i) % 200 for i in range(140)], [i % 4 for i in range(140)], 4, 1, 128, 32, 50),
 ]
 
 
@@ -391,6 +430,45 @@ def test_attention_bad_indices_are_reported_and_left_out(dev, mosaic):
     assert mosaic.mq_get_error() == 1  # rows past T
     within(o[0], good[0][0], bound[0], "the first sequence")
     assert (o[1] == 77).all()
+
+
+def test_attention_shapes_share_a_workspace(dev, mosaic):
+    """Calls of different shapes take turns on one workspace, large enough for each: the partial
+    sums of one leave the other's counters alone."""
+    runs = []
+    for k, (lens, nqs, Hq, H, D) in enumerate((([5000, 3000], [1, 1], 8, 1, 128), ([2600], [9], 4, 1, 64), ([4100], [6], 8, 2, 128))):
+        q, pages, ks, vs, table, kv_len, cu = attn_inputs(lens, nqs, Hq, H, D, 32, BF, 60 + k, dev)
+        want = ref.attention(q, pages, ks, vs, table, lens, nqs, 0.1, 0)
+        runs.append((q, pages, ks, vs, table, kv_len, cu, max(nqs), want, attn_bounds(*want, BF, lens)[0]))
+    need = max(mosaic.kv_attention_workspace(r[0], mosaic.KVCache(*r[1:4]), r[7]).numel() for r in runs)
+    ws = torch.zeros(need, dtype=torch.uint8, device=dev)
+    for _ in range(3):
+        for q, pages, ks, vs, table, kv_len, cu, most, want, bound in runs:
+            o, _ = run_attn(mosaic, q, pages, ks, vs, table, kv_len, cu, most, 0.1, 0, BF, ws=ws)
+            within(o, want[0], bound)
+
+
+def test_cache_past_32_bits(dev, mosaic):
+    """Slots whose bytes lie past 2^32 of the cache, written, read back and attended to."""
+    H, D, P = 8, 128, 64
+    per_page = mosaic.lib().mq_kv_cache_bytes(1, P, H, D)
+    pages = 2 ** 32 // per_page + 40
+    cache = mosaic.KVCache(torch.empty((pages, H, P // 16, 18 * D), dtype=torch.uint8, device=dev))
+    n = 150
+    table = torch.tensor([[pages - 1, pages - 17, pages - 3]], dtype=torch.int32, device=dev)
+    tok = torch.arange(n, device=dev)
+    slots = table[0, tok // P].long() * P + tok % P
+    gen = torch.Generator().manual_seed(5)
+    k, v = (torch.randn(n, H, D, generator=gen).to(BF).to(dev) for _ in range(2))
+    mosaic.mq_kv_append(k, v, slots, cache)
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    mosaic.mq_kv_read(cache, slots, ko, vo)
+    for x, got in ((k, ko), (v, vo)):
+        assert torch.equal(got.cpu(), torch.from_numpy(oracle_rows(x, None)[2]).to(BF))
+    q = torch.randn(1, 16, D, generator=gen).to(BF).to(dev)
+    want = ref.attention(q, cache.pages, None, None, table, [n], [1], 0.09, 0)
+    o, _ = run_attn(mosaic, q, cache.pages, None, None, table, torch.tensor([n], dtype=torch.int32, device=dev), None, 1, 0.09, 0, BF, False)
+    within(o, want[0], attn_bounds(*want, BF, [n])[0])
 
 
 def test_attention_leaves_other_rows(dev, mosaic):
