@@ -6,9 +6,10 @@
 // The work of 64 weight rows is a list of steps: 256 columns of the base each, then four
 // residual blocks each (a block row's blocks lie one behind the other). In both a lane of
 // a warp takes 64 adjacent columns of its rows, at a column of its own, which a product's
-// free order of k allows; so a residual step is as dense as a base step. A step's codes
+// free order of k allows; so a residual step is as dense as a base step. Two warps share a step,
+// each with half of every lane's columns: 16 warps an SM with 160 KB of rings. A step's codes
 // (8 KB, one TMA box, 128-byte swizzle; or four packed blocks, one bulk copy) and scales
-// (2 KB, one bulk copy) go to the warp's own ring in shared memory.
+// (2 KB, one bulk copy) go to the pair's own ring in shared memory.
 //
 // The weights are the 16-row operand of fp16 tensor-core products (val * dec(sf) is exact
 // in fp16), eight tokens the other one. A first kernel writes the activations as that operand: in
@@ -18,7 +19,7 @@
 // 14336 x 4096: 28.3 us against 18.3; one through 28672 x 8192: 45.1 against 43.4). The two kernels overlap: the weight's copies do not wait for
 // the first one.
 //
-// The steps of a row tile are dealt to the warps of a cluster of S CTAs, S so that the CTAs
+// The steps of a row tile are dealt to the pairs of a cluster of S CTAs, S so that the CTAs
 // about fill the GPU; the warps' sums are added in their order through shared memory, then
 // the CTAs' through the cluster's.
 #include <algorithm>
@@ -30,8 +31,9 @@ namespace mq {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
+// Pairs of warps of a CTA: what 128 and 168 registers a thread leave room for, two CTAs an SM.
+template <int NT>
+__host__ __device__ constexpr int pairs() { return NT == 1 ? 4 : 3; }
 constexpr int kStages = 2;
 constexpr int kRows = 64;              // weight rows of a tile (a block row)
 constexpr int kCols = 256;             // base columns of a step
@@ -41,7 +43,8 @@ constexpr int kCtasPerSm = 2;
 constexpr int kXThreads = 512, kXKeep = 4;  // of the operand's kernel: 16384 columns are read once
 constexpr int kPitch = kRows + 4;      // floats of a token's row in the sums
 
-constexpr size_t smem_bytes() { return (size_t)kWarps * (kStages * kStage + kStages * 8); }
+template <int NT>
+constexpr size_t smem_bytes() { return (size_t)pairs<NT>() * kStages * (kStage + 16); }
 
 // Bytes of the operand: per 64-column chunk and eight tokens 1 KB, [piece of 8 columns][token], and
 // every token's scale.
@@ -102,14 +105,20 @@ __global__ void __launch_bounds__(kXThreads) k_gemv_x(const uint16_t* __restrict
 }
 
 template <int NT, bool F16>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) k_gemv(const __grid_constant__ CUtensorMap tw, const GemvParams p) {
+__global__ void __launch_bounds__(64 * pairs<NT>(), kCtasPerSm) k_gemv(const __grid_constant__ CUtensorMap tw, const GemvParams p) {
     // The swizzle's pattern repeats every 1024 bytes. Without static shared memory the array
     // starts on such a boundary (checked below), and two CTAs fit an SM.
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint64_t(*full)[kStages] = reinterpret_cast<uint64_t(*)[kStages]>(smem + kWarps * kStages * kStage);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    constexpr int kPairs = pairs<NT>(), kWarps = 2 * kPairs, kThreads = 32 * kWarps;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pair = warp >> 1, h = warp & 1, g = lane >> 2, t = lane & 3;
+    // per pair and stage: its copies have landed, both warps are done with it
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairs * kStages * kStage) + pair * (2 * kStages);
+    uint64_t* empty = full + kStages;
     const int tile = blockIdx.y, S = gridDim.x, rank = blockIdx.x, KC = p.K / 64;
-    if (tid < kWarps * kStages) mbar_init(&full[0][0] + tid, 1);
+    if (h == 0 && lane < kStages) {
+        mbar_init(full + lane, 1);
+        mbar_init(empty + lane, 2);
+    }
     mbar_fence_init();
     if (tid == 0) tma_prefetch_desc(&tw);
     __syncthreads();
@@ -117,15 +126,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_gemv(const __grid_cons
         if (tid == 0) report_index(p.err);
         return;
     }
-    const int nbase = p.base ? (KC + 3) / 4 : 0, step0 = rank * kWarps + warp, stride = S * kWarps;
-    uint8_t* ring = smem + warp * (kStages * kStage);
+    const int nbase = p.base ? (KC + 3) / 4 : 0, step0 = rank * kPairs + pair, stride = S * kPairs;
+    uint8_t* ring = smem + pair * (kStages * kStage);
     int res0 = 0, res1 = 0;
 
     auto issue = [&](int i) {
-        if (lane == 0) {
+        if (h == 0 && lane == 0) {
             const int step = step0 + i * stride;
             uint8_t* dst = ring + (i % kStages) * kStage;
-            uint64_t* bar = &full[warp][i % kStages];
+            uint64_t* bar = full + i % kStages;
             if (step < nbase) {
                 const uint32_t sf = (uint32_t)min(4, KC - 4 * step) * 512;
                 mbar_arrive_expect_tx(bar, kCodes + sf);
@@ -159,12 +168,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_gemv(const __grid_cons
         const int e = res0 + 4 * (step - nbase) + c;
         return e < res1 ? __ldg(p.blk_kt + e) : -1;
     };
-    int kt = steps > 0 ? chunk_of(0, t) : -1, ktn = steps > 1 ? chunk_of(1, t) : -1;
+    const int kt = steps > 0 ? chunk_of(0, t) : -1;
+    int ktn = steps > 1 ? chunk_of(1, t) : -1;
     griddep_wait();
     griddep_launch();
 
-    uint4 b[NT][4];  // the lane's operand in 32 of its 64 columns, half a step ahead
-    auto load_x = [&](int kt, int h) {
+    uint4 b[NT][4];  // the lane's operand in the warp's 32 of its 64 columns, a step ahead
+    auto load_x = [&](int kt) {
         const uint8_t* src = p.xop + (int64_t)kt * (NT * 1024) + (4 * h) * 128 + g * 16;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -172,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_gemv(const __grid_cons
             for (int w = 0; w < 4; ++w)
                 b[nt][w] = kt >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + nt * 1024 + w * 128)) : make_uint4(0, 0, 0, 0);
     };
-    load_x(kt, 0);
+    load_x(kt);
 
     float acc[4][NT][4];
 #pragma unroll
@@ -188,39 +198,37 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_gemv(const __grid_cons
         const bool valid = step < nbase ? 4 * step + t < KC : res0 + 4 * (step - nbase) + t < res1;  // columns of this lane's rows
         const uint32_t parity = (i / kStages) & 1u;
         // the warp decides together; after a wait that gave up (reported) nothing is issued or waited for
-        if (__any_sync(0xffffffffu, !mbar_try_wait(&full[warp][i % kStages], parity)) && alive)
-            alive = __all_sync(0xffffffffu, mbar_wait_err(&full[warp][i % kStages], parity, p.err));
+        if (__any_sync(0xffffffffu, !mbar_try_wait(full + i % kStages, parity)) && alive)
+            alive = __all_sync(0xffffffffu, mbar_wait_err(full + i % kStages, parity, p.err));
         const uint8_t* buf = ring + (i % kStages) * kStage;
         // scales of rows 16 rt + 8 hf + g in the lane's 64 columns: a 128-row chunk holds row
         // r's four at (r % 32) * 16 + (r / 32) * 4. Columns past the end may hold anything: zero.
-        uint32_t sc[4][2][2];
+        uint32_t sc[4][2];  // the warp's half: two groups of 16 columns
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                uint2 w = *reinterpret_cast<const uint2*>(buf + kCodes + t * 512 + (16 * q + 8 * hf + g) * 16 + (tile & 1) * 8);
-                if (!valid) w = make_uint2(0, 0);
-                e4m3x4_half(w.x, sc[q][hf][0], sc[q][hf][1]);
-                e4m3x4_half(w.y, sc[q + 2][hf][0], sc[q + 2][hf][1]);
+                const uint2 w = *reinterpret_cast<const uint2*>(buf + kCodes + t * 512 + (16 * q + 8 * hf + g) * 16 + (tile & 1) * 8);
+                const uint32_t two = __byte_perm(w.x, w.y, h ? 0x7632 : 0x5410);
+                e4m3x4_half(valid ? two : 0u, sc[q][hf], sc[q + 2][hf]);
             }
         // 16-byte piece h of the lane's columns in row r: swizzled rows of 128 bytes, or packed blocks
         const bool isb = step < nbase;
         const uint8_t* codes = isb ? buf + g * 128 : buf + t * 2048 + g * 16;
         const int row8 = isb ? 1024 : 256;  // eight rows further
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
+        {
             const uint8_t* at = codes + (isb ? ((2 * t + h) ^ g) * 16 : h * 128);
             uint4 x0[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int w = 0; w < 4; ++w) x0[nt][w] = b[nt][w];
-            load_x(h ? ktn : kt, h ^ 1);
+            load_x(ktn);
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) {
                 const uint4 a0 = *reinterpret_cast<const uint4*>(at + (2 * rt) * row8);
                 const uint4 a1 = *reinterpret_cast<const uint4*>(at + (2 * rt + 1) * row8);
-                const uint32_t s0 = h ? sc[rt][0][1] : sc[rt][0][0], s1 = h ? sc[rt][1][1] : sc[rt][1][0];
+                const uint32_t s0 = sc[rt][0], s1 = sc[rt][1];
                 const uint32_t w0[4] = {a0.x, a0.y, a0.z, a0.w}, w1[4] = {a1.x, a1.y, a1.z, a1.w};
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
@@ -239,14 +247,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_gemv(const __grid_cons
                 }
             }
         }
-        kt = ktn;
         ktn = i + 2 < steps ? chunk_of(i + 2, t) : -1;
         __syncwarp();
-        if (i + kStages < steps && alive) issue(i + kStages);
+        if (lane == 0) mbar_arrive(empty + i % kStages);
+        if (h == 0 && i + kStages < steps && alive) {
+            // the other warp's half
+            if (__any_sync(0xffffffffu, !mbar_try_wait(empty + i % kStages, parity)))
+                alive = __all_sync(0xffffffffu, mbar_wait_err(empty + i % kStages, parity, p.err));
+            if (alive) issue(i + kStages);
+        }
     }
     if (!alive)  // the last copies get their (bounded) time
-        for (int i = max(0, steps - kStages); i < steps; ++i)
-            mbar_wait_err(&full[warp][i % kStages], (i / kStages) & 1u, p.err);
+        for (int i = max(0, steps - kStages); i < steps; ++i) mbar_wait_err(full + i % kStages, (i / kStages) & 1u, p.err);
 
     // the warps' sums, then the CTAs', each in order
     __syncthreads();
@@ -288,14 +300,14 @@ template <int NT, bool F16>
 cudaError_t gemv_of(const CUtensorMap& tw, const GemvParams& p, int S, cudaStream_t s) {
     static std::atomic<bool> done[64];
     cudaError_t e = once_per_device(done, [] {
-        return cudaFuncSetAttribute(k_gemv<NT, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes());
+        return cudaFuncSetAttribute(k_gemv<NT, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<NT>());
     });
     if (e != cudaSuccess) return e;
     uint8_t* xop = p.xop;
     e = launch_pdl(k_gemv_x<F16>, dim3(8 * NT), dim3(kXThreads), 0, s, 1, p.X, p.ldx, p.M, NT, p.K, xop,
                    reinterpret_cast<float*>(xop + (int64_t)(p.K / 64) * (NT * 1024)));
     if (e != cudaSuccess) return e;
-    return launch_pdl_cluster(k_gemv<NT, F16>, dim3(S, p.N / kRows), dim3(kThreads), smem_bytes(), s, dim3(S, 1, 1), tw, p);
+    return launch_pdl_cluster(k_gemv<NT, F16>, dim3(S, p.N / kRows), dim3(64 * pairs<NT>()), smem_bytes<NT>(), s, dim3(S, 1, 1), tw, p);
 }
 
 }  // namespace
@@ -305,7 +317,7 @@ size_t gemv_workspace(int M, int K) { return operand_bytes(M <= 8 ? 1 : 2, K); }
 cudaError_t launch_gemv(const CUtensorMap& tw, const GemvParams& p, bool f16, cudaStream_t s) {
     const int tiles = p.N / kRows, steps = (p.K / 64 + 3) / 4;
     // CTAs that fill the GPU once, none without a step for each of its warps
-    const int S = std::max(1, std::min({8, kCtasPerSm * device_sms() / tiles, steps / kWarps}));
+    const int S = std::max(1, std::min({8, kCtasPerSm * device_sms() / tiles, steps / (p.M <= 8 ? pairs<1>() : pairs<2>())}));
     if (p.M <= 8) return f16 ? gemv_of<1, true>(tw, p, S, s) : gemv_of<1, false>(tw, p, S, s);
     return f16 ? gemv_of<2, true>(tw, p, S, s) : gemv_of<2, false>(tw, p, S, s);
 }
