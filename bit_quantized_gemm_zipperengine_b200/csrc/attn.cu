@@ -800,8 +800,13 @@ cudaError_t attn_of(const AttnParams& p, int grid, cudaStream_t s) {
     return launch_pdl(k_attn<D, NT, F16>, dim3(grid), dim3(kThreads), smem, s, 1, p);
 }
 
+// Eights of query rows that a CTA holds. More rows share a step's conversions, up to what the
+// registers hold; with few rows the shorter step wins (8 sequences of up to 4001 tokens and 24
+// rows: 26.4 us by 16, 29.0 by 24; 512 rows: 157 and 143 us; 2 x 2048 rows behind 8192
+// tokens: 661 and 598 us).
 int row_tiles(int q_heads, int kv_heads, int max_q) {
-    return (int64_t)(q_heads / kv_heads) * max_q <= 8 ? 1 : 2;
+    const int64_t rows = (int64_t)(q_heads / kv_heads) * max_q;
+    return rows <= 8 ? 1 : rows <= 32 ? 2 : 3;
 }
 
 int grid_of(int nt) { return device_sms() * (nt == 1 ? ctas_per_sm<1>() : ctas_per_sm<2>()); }
@@ -825,9 +830,11 @@ cudaError_t launch_attn(const AttnParams& p0, int D, int max_q, bool f16, cudaSt
     p.by_grid = FastDiv(grid);
     if (D == 64) {
         if (nt == 1) return f16 ? attn_of<64, 1, true>(p, grid, s) : attn_of<64, 1, false>(p, grid, s);
+        if (nt == 3) return f16 ? attn_of<64, 3, true>(p, grid, s) : attn_of<64, 3, false>(p, grid, s);
         return f16 ? attn_of<64, 2, true>(p, grid, s) : attn_of<64, 2, false>(p, grid, s);
     }
     if (nt == 1) return f16 ? attn_of<128, 1, true>(p, grid, s) : attn_of<128, 1, false>(p, grid, s);
+    if (nt == 3) return f16 ? attn_of<128, 3, true>(p, grid, s) : attn_of<128, 3, false>(p, grid, s);
     return f16 ? attn_of<128, 2, true>(p, grid, s) : attn_of<128, 2, false>(p, grid, s);
 }
 

@@ -367,7 +367,8 @@ mq_status mq_gemm_noalloc(const mq_nvfp4_mat* xq, const mq_nvfp4_mat* wq, const 
 size_t mq_gemm_noalloc_scratch_limit(void);
 
 /* Synchronizes `stream`, then returns (and clears) the device error word: MQ_OK, or
- * MQ_ERR_TIMEOUT if a kernel gave up on a pipeline wait, or MQ_ERR_CUDA if the
+ * MQ_ERR_TIMEOUT if a kernel gave up on a pipeline wait, or MQ_ERR_INVALID_ARG if an operator
+ * of mosaic_ops.h met an index out of range (whichever came first), or MQ_ERR_CUDA if the
  * synchronization itself failed. */
 mq_status mq_get_error(mq_stream stream);
 
