@@ -214,7 +214,8 @@ mq_status mq_kv_attention(const mq_heads* q, const mq_heads* out, float* lse, in
     p.cu_q = cu_q;
     p.kv_len = kv_len;
     p.scale = scale;
-    p.window = window;
+    // from the longest length on a window holds everything (and the kernel's sums stay in 32 bits)
+    p.window = window < (1 << 30) ? window : 0;
     p.counters = static_cast<int*>(ws);
     p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + partials_at);
     p.err = device_error_word();

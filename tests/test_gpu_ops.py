@@ -393,6 +393,16 @@ def test_attention_sharp_flat_and_odd_scales(qmul, scale, dev, mosaic):
     within(lse, want[1], bl, "lse")
 
 
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 30, 2 ** 30 - 1])
+def test_attention_huge_windows(window, dev, mosaic):
+    """A window that holds every token, with more query tokens than cached ones, is no window."""
+    lens, nqs = [2, 40, 0], [5, 2, 3]
+    q, pages, ks, vs, table, kv_len, cu = attn_inputs(lens, nqs, 8, 2, 64, 16, BF, 12, dev)
+    want = run_attn(mosaic, q, pages, ks, vs, table, kv_len, cu, 5, 0.125, 0, BF)
+    got = run_attn(mosaic, q, pages, ks, vs, table, kv_len, cu, 5, 0.125, window, BF)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_attention_query_beyond_fp16(dev, mosaic):
     """bf16 queries far above and below fp16's range, with a scale that brings the scores back."""
     lens, nqs = [300], [4]
