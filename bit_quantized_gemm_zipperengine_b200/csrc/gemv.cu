@@ -155,18 +155,22 @@ __global__ void __launch_bounds__(64 * pairs<NT>(), kCtasPerSm) k_gemv(const __g
     int ahead = 0;
     while (ahead < kStages && step0 + ahead * stride < nbase) issue(ahead++);
     if (p.blk_codes) {
-        res0 = __ldg(p.tile_ptr + tile);
-        res1 = __ldg(p.tile_ptr + tile + 1);
+        const int e0 = __ldg(p.tile_ptr + tile), e1 = __ldg(p.tile_ptr + tile + 1);
+        res0 = min(max(e0, 0), p.nblk);  // a well-formed range is inside the store
+        res1 = min(max(e1, res0), p.nblk);
+        if ((res0 != e0 || res1 != e1) && tid == 0) report_index(p.err);
     }
     const int total = nbase + (res1 - res0 + 3) / 4;
     const int steps = step0 < total ? (total - step0 + stride - 1) / stride : 0;
     while (ahead < min(kStages, steps)) issue(ahead++);
-    // Column chunk c (0..3, 64 columns) of a step, -1 past the end.
+    // Column chunk c (0..3, 64 columns) of a step, -1 past the end (a block's: or past K).
     auto chunk_of = [&](int i, int c) {
         const int step = step0 + i * stride;
         if (step < nbase) return 4 * step + c < KC ? 4 * step + c : -1;
         const int e = res0 + 4 * (step - nbase) + c;
-        return e < res1 ? __ldg(p.blk_kt + e) : -1;
+        const int kt = e < res1 ? __ldg(p.blk_kt + e) : -1;
+        if (e < res1 && (unsigned)kt >= (unsigned)KC) report_index(p.err);
+        return (unsigned)kt < (unsigned)KC ? kt : -1;
     };
     const int kt = steps > 0 ? chunk_of(0, t) : -1;
     int ktn = steps > 1 ? chunk_of(1, t) : -1;

@@ -84,6 +84,7 @@ mq_status mq_gemv(const void* X, mq_dtype type, int64_t ldx, const mq_nvfp4_mat*
         p.blk_sf = r->blk_sf;
         p.blk_kt = r->blk_kt;
         p.tile_ptr = r->tile_ptr;
+        p.nblk = r->nblk;
     }
     p.Y = static_cast<uint16_t*>(Y);
     p.ldy = M > 1 ? ldy : 0;

@@ -98,6 +98,7 @@ struct GemvParams {
     const float* g_w;
     const uint8_t *blk_codes, *blk_sf;  // null: no residual
     const int32_t *blk_kt, *tile_ptr;
+    int nblk;
     uint16_t* Y;
     int64_t ldy;
     int M, N, K;

@@ -74,7 +74,8 @@ size_t mq_kv_cache_bytes(int num_pages, int page_size, int heads, int D);
  * m * ldx elements (16-byte aligned, ldx % 8 == 0); Y: [M][N], row m at m * ldy.
  * 1 <= M <= 16 tokens (MQ_ERR_UNSUPPORTED_SHAPE above: mq_gemm serves those), any N and K
  * that are multiples of 64. wq: codes, sf_swz (both 16-byte aligned), gscale [1]. r as in
- * mq_gemm, with blk_kt. flags: 0 or MQ_GEMM_BASE_ONLY / MQ_GEMM_RESIDUAL_ONLY;
+ * mq_gemm, with blk_kt; blocks that tile_ptr puts past the store and columns that blk_kt puts
+ * past K are left out and reported. flags: 0 or MQ_GEMM_BASE_ONLY / MQ_GEMM_RESIDUAL_ONLY;
  * MQ_GEMM_WEIGHTS_READY is taken and changes nothing (the weight is read while the activations
  * are prepared in any case). Repeated calls give the same bits. ws: mq_gemv_workspace_bytes,
  * 16-byte aligned, any contents; calls that share one must not overlap on the GPU.

@@ -91,6 +91,24 @@ def test_gemv_parts_strides_flags(mode, dev, mosaic):
         assert torch.equal(first, y)
 
 
+def test_gemv_bad_block_indices_are_reported_and_left_out(dev, mosaic):
+    """Ranges past the packed store and columns past K meet the kernel's own checks."""
+    N, K, M = 192, 320, 3
+    base, packed = ref.random_weight(N, K, 7, 5, dev)
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(9)).to(BF).to(dev)
+    good = torch.empty(M, N, dtype=BF, device=dev)
+    mosaic.mq_gemv(x, mosaic.Weight(base, packed), good)
+    for field, at, bad in (("tile_ptr", 3, 2 ** 31 - 1), ("tile_ptr", 2, -5), ("blk_kt", 6, K // 64), ("blk_kt", 6, -1),
+                           ("blk_kt", 6, 2 ** 31 - 1)):
+        p = dict(packed)
+        p[field] = packed[field].clone()
+        p[field][at] = bad
+        y = torch.empty_like(good)
+        mosaic.mq_gemv(x, mosaic.Weight(base, p), y)
+        assert mosaic.mq_get_error() == 1, (field, bad)
+        assert torch.isfinite(y).all() and torch.equal(y[:, :64], good[:, :64])
+
+
 @pytest.mark.parametrize("big", [1e-30, 1e30])
 def test_gemv_far_magnitudes(big, dev, mosaic):
     """bf16 activations far outside fp16's range, and rows of very different size."""
