@@ -14,8 +14,11 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 bool heads_ok(const mq_heads* h, int T, int D, bool output) {
     if (!h || !h->data || !aligned(h->data, 16) || h->heads <= 0 || h->heads > (1 << 20)) return false;
     if (h->token_stride < 0 || h->head_stride < 0 || h->token_stride % 8 || h->head_stride % 8) return false;
-    if (output && ((T > 1 && h->token_stride < D) || (h->heads > 1 && h->head_stride < D))) return false;
-    return true;
+    if (!output || T <= 0) return true;
+    // one axis inside the other: its rows side by side, and all of them before the next one's
+    const int64_t n[2] = {T, h->heads}, s[2] = {T > 1 ? h->token_stride : INT64_MAX, h->heads > 1 ? h->head_stride : INT64_MAX};
+    const int in = s[0] < s[1] ? 0 : 1, out = 1 - in;
+    return (n[in] == 1 || s[in] >= D) && (n[out] == 1 || (s[out] - D) / (n[in] - 1) >= s[in]);
 }
 
 HeadsView view(const mq_heads* h) {

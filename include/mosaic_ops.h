@@ -28,7 +28,8 @@ typedef enum {
 /*
  * A [tokens][heads][D] tensor: element (t, h, d) at data + t * token_stride +
  * h * head_stride + d (strides in elements, >= 0; the D elements are adjacent). data and
- * both strides must be multiples of 16 bytes.
+ * both strides must be multiples of 16 bytes. Rows of an output must not overlap: one axis
+ * lies inside a step of the other.
  */
 typedef struct {
     void* data;

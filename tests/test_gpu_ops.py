@@ -215,6 +215,21 @@ def test_norm_rope(T, Hq, Hk, D, rot, norm, inter, dtype, dev, mosaic):
     assert torch.equal(q, qo) and torch.equal(k, ko)
 
 
+@pytest.mark.parametrize("T,Hq", [(5, 3), (1, 4), (6, 1)])
+def test_norm_rope_output_layouts(T, Hq, dev, mosaic):
+    """Tokens inside heads, heads inside tokens, gaps, and axes of one element with stride 0."""
+    D = 64
+    q = torch.randn(T, Hq, D, generator=torch.Generator().manual_seed(4)).to(BF).to(dev)
+    pos, freq = torch.arange(T, device=dev), (1e4 ** (-2.0 * torch.arange(D // 2, dtype=torch.float64) / D)).to(dev)
+    want = torch.empty_like(q)
+    mosaic.mq_qk_norm_rope(q, None, want, None, pos, freq)
+    mem = torch.empty(T * Hq * D * 4, dtype=BF, device=dev)
+    for st, sh in ((D, T * D), (Hq * D, D), (Hq * (D + 8) + 16, D + 8), (D + 8, T * (D + 8)), (0 if T == 1 else Hq * D, 0 if Hq == 1 else D)):
+        o = mem.as_strided((T, Hq, D), (st, sh, 1))
+        mosaic.mq_qk_norm_rope(q, None, o, None, pos, freq)
+        assert torch.equal(o, want), (st, sh)
+
+
 def test_rope_far_positions_and_zero_rows(dev, mosaic):
     q, k, _, w, pos, freq = rope_inputs(8, 2, 1, 128, HF, 3, dev)
     pos = torch.tensor([0, 1, -5, 2 ** 20, 2 ** 31, 2 ** 40, -(2 ** 33), 7], device=dev)

@@ -126,6 +126,18 @@ def test_rope_and_append_refusals(L, buf):
     assert both(rot=24) == 1 and both(k=heads(mem, 1, D, D)) == 1 and both(ko=heads(mem, 1, D, D)) == 1
 
 
+def test_outputs_whose_rows_overlap_are_refused(L, buf):
+    T, D, mem = 4, 64, buf(1 << 14)
+    q = heads(mem, 3, 3 * D, D)
+
+    def rope(qo, T=T, q=q):
+        return L.mq_qk_norm_rope(q, None, qo, None, T, D, 0, None, None, 1e-6, None, None, 0, 0, None)
+
+    for token, head in ((D, D), (2 * D, D), (3 * D - 8, D), (D, 4 * D - 8), (D, 3 * D), (3 * D, D - 8), (D - 8, 8 * D)):
+        assert rope(heads(mem, 3, token, head)) == 1, (token, head)
+    assert rope(heads(mem, 3, 0, D - 8), T=1) == 1 and rope(heads(mem, 1, D - 8, 0), q=heads(mem, 1, D, D)) == 1
+
+
 def test_attention_refusals(L, buf):
     from bit_quantized_gemm_zipperengine_b200 import mosaic
     T, D, B = 3, 64, 3
