@@ -125,7 +125,7 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 // ln of the sum of 2^z, kept as sum = sum of 2^(z - top + kShift).
 __device__ __forceinline__ float lse_of(float top, float sum) {
-    return sum > 0.0f ? (top - kShift + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+    return sum == 0.0f ? -INFINITY : (top - kShift + log2f(sum)) * 0.69314718055994531f;
 }
 
 template <int D, int NT, bool F16>
@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
                     for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm_m[w][row]);
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w)
-                        sum += sm_m[w][row] == -INFINITY ? 0.0f : sm_l[w][row] * ex2(sm_m[w][row] - top);
+                        sum += sm_l[w][row] * (sm_m[w][row] == -INFINITY ? 0.0f : ex2(sm_m[w][row] - top));
                     dst[R * D + row] = top;
                     dst[R * D + R + row] = sum;
                 }
@@ -700,11 +700,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
                     const float2 v = reinterpret_cast<const float2*>(merge + (w * R + row) * RS)[8 * pj + pg];
                     a.x += v.x;
                     a.y += v.y;
-                    sum += sm_m[w][row] == -INFINITY ? 0.0f : sm_l[w][row] * ex2(sm_m[w][row] - top);
+                    sum += sm_l[w][row] * (sm_m[w][row] == -INFINITY ? 0.0f : ex2(sm_m[w][row] - top));
                 }
                 const int qi = (int)G.div(r0 + row), hq = h * G.d + r0 + row - qi * G.d;
                 const int64_t tok = s.row0 + qi;
-                const float inv = sum > 0.0f ? gv / sum : 0.0f;
+                const float inv = sum == 0.0f ? 0.0f : gv / sum;
                 *reinterpret_cast<uint32_t*>(p.o.p + tok * p.o.st + hq * p.o.sh + 2 * pi) = narrow2<F16>(a.x * inv, a.y * inv);
                 if (p.lse && pi == 0) p.lse[tok * p.q.heads + hq] = lse_of(top, sum);
             }
@@ -764,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
                 }
                 const int qi = (int)G.div(r0 + row), hq = h * G.d + r0 + row - qi * G.d;
                 const int64_t tok = s.row0 + qi;
-                const float sum = sm_l[0][row], inv = sum > 0.0f ? gv / sum : 0.0f;
+                const float sum = sm_l[0][row], inv = sum == 0.0f ? 0.0f : gv / sum;
                 *reinterpret_cast<uint2*>(p.o.p + tok * p.o.st + hq * p.o.sh + d) =
                     make_uint2(narrow2<F16>(a.x * inv, a.y * inv), narrow2<F16>(a.z * inv, a.w * inv));
                 if (p.lse && d == 0) p.lse[tok * p.q.heads + hq] = lse_of(sm_m[0][row], sum);

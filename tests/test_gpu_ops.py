@@ -451,6 +451,25 @@ def test_attention_query_beyond_fp16(dev, mosaic):
         within(lse, want[1], bl, "lse")
 
 
+def test_attention_nan_queries(dev, mosaic):
+    """A query row that holds a NaN gives NaN for itself, its lse too, and for no other row."""
+    lens, nqs = [1500, 40, 0], [1, 3, 1]
+    q, pages, ks, vs, table, kv_len, cu = attn_inputs(lens, nqs, 8, 2, 128, 16, BF, 22, dev)
+    want = ref.attention(q, pages, ks, vs, table, lens, nqs, 0.1, 0)
+    bo, bl = attn_bounds(*want, BF, lens)
+    q = q.contiguous()
+    for t, h in ((0, 3), (2, 6), (4, 1)):
+        q[t, h, 17] = math.nan
+    o, lse = run_attn(mosaic, q, pages, ks, vs, table, kv_len, cu, 3, 0.1, 0, BF)
+    hit = torch.zeros(o.shape[:2], dtype=torch.bool, device=dev)
+    hit[0, 3] = hit[2, 6] = True  # the third sees nothing: zeros
+    assert torch.isnan(o[hit]).all() and torch.isnan(lse[hit]).all()
+    within(o[~hit], want[0][~hit], bo[~hit], "the other rows")
+    dead = want[1] == -math.inf
+    assert (lse[dead] == -math.inf).all() and (o[dead] == 0).all()
+    within(lse[~hit & ~dead], want[1][~hit & ~dead], bl[~hit & ~dead], "lse")
+
+
 def test_attention_bad_indices_are_reported_and_left_out(dev, mosaic):
     """Bad pages, lengths and rows meet the kernels' own checks: their tokens are left out."""
     lens, nqs = [100, 40], [1, 1]
