@@ -546,10 +546,12 @@ class Layer:
 
     def forward_16bit(self, X: torch.Tensor, out: torch.Tensor | None = None, flags: int = 0, stream=None):
         """X [M][K] in bf16 or fp16, M <= 16, times the packed weight without quantizing X
-        (mq_gemv): a new tensor, or out."""
-        Y = torch.empty((X.shape[0], self.N), dtype=X.dtype, device=X.device) if out is None else out
-        mq_gemv(X, self.weight, Y, flags, stream)
-        return Y
+        (mq_gemv): a new tensor (of stream's memory pool), or out."""
+        if out is None:
+            with torch.cuda.stream(stream):
+                out = torch.empty((X.shape[0], self.N), dtype=X.dtype, device=X.device)
+        mq_gemv(X, self.weight, out, flags, stream)
+        return out
 
 
 class AttentionLayer:
@@ -578,15 +580,26 @@ class AttentionLayer:
             raise MosaicError("more than 16 tokens are taken in bf16")
         return layer.forward(X)
 
-    def step(self, X, pos, slots, block_table, kv_len, cu_q=None, max_q: int = 1, stream=None):
+    def _workspace(self, q, max_q):
+        # A captured call gets its own, zeroed at every replay: one kept here would be shared by
+        # graphs that may run together, and be zeroed by the first one only.
+        if torch.cuda.is_current_stream_capturing():
+            return kv_attention_workspace(q, self.cache, max_q)
+        key = (max_q, torch.cuda.current_stream(q.device))
+        if key not in self._ws:
+            self._ws[key] = kv_attention_workspace(q, self.cache, max_q)
+        return self._ws[key]
+
+    def step(self, X, pos, slots, block_table, kv_len, cu_q=None, max_q: int = 1, stream=None, ws=None):
         """One pass of the T new tokens X [T][hidden] (bf16; fp16 up to 16 tokens): their keys
         and values are appended at slots, then they attend to their sequences. kv_len counts
-        them. Tokens of one sequence are adjacent (cu_q). Every stream has its own workspace,
-        so calls of up to 16 tokens may overlap on different streams; calls of more tokens use
-        the layers' own buffers (see Layer.forward) and must not."""
+        them. Tokens of one sequence are adjacent (cu_q). Every stream and every captured call
+        has its own workspace (ws: kv_attention_workspace(q, cache, max_q) of the caller's), so
+        calls of up to 16 tokens may overlap on different streams; calls of more tokens use the
+        layers' own buffers (see Layer.forward) and must not."""
         if stream is not None:
             with torch.cuda.stream(stream):
-                return self.step(X, pos, slots, block_table, kv_len, cu_q, max_q)
+                return self.step(X, pos, slots, block_table, kv_len, cu_q, max_q, None, ws)
         T, D, H, Hq = X.shape[0], self.cache.D, self.cache.heads, self.q_heads
         if T == 0:
             return X.new_empty((0, self.out.N))
@@ -595,9 +608,6 @@ class AttentionLayer:
         mq_qkv_append(q, k, v, q, slots, self.cache, pos, self.freq, self.q_norm, self.k_norm, self.eps,
                       self.interleaved)
         o = torch.empty((T, Hq, D), dtype=X.dtype, device=X.device)
-        key = (max_q, torch.cuda.current_stream(X.device))
-        if key not in self._ws:
-            self._ws[key] = kv_attention_workspace(q, self.cache, max_q)
         mq_kv_attention(q, self.cache, block_table, kv_len, o, self.scale, cu_q, max_q, self.window, None,
-                        self._ws[key])
+                        self._workspace(q, max_q) if ws is None else ws)
         return self._project(self.out, o.view(T, Hq * D))

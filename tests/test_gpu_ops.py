@@ -628,3 +628,42 @@ def test_attention_layer(norm, dev, mosaic):
 
     for nqs in ([23, 17], [1, 1], [1, 1], [3, 1], [0, 2], [9, 1]):
         step(nqs)
+
+
+def test_attention_layer_in_graphs(dev, mosaic):
+    """Two captured steps of one layer and eager ones, in any order and at once: each has a
+    workspace of its own, and a graph replayed first is not the one that was captured first."""
+    Hq, H, D, hidden, P, n = 8, 1, 64, 128, 32, 3000
+    qkv, proj = mosaic.Layer((Hq + 2 * H) * D, hidden, 3, dev), mosaic.Layer(hidden, Hq * D, 2, dev)
+    for i, l in enumerate((qkv, proj)):
+        l.prepare_path(to_dev(synth.weight(l.N, l.K, 90 + i, 94, 0.06, 40, 2, 8.0), dev), to_dev(synth.act(128, l.K, 96 + i, 98, 4, 5.0), dev))
+    pages, _, _ = ref.random_cache(2 * (-(-n // P) + 1), P, H, D, 6, dev, False)
+    freq = (1e4 ** (-2.0 * torch.arange(D // 2, dtype=torch.float64) / D)).to(dev)
+    layer = mosaic.AttentionLayer(qkv, proj, Hq, mosaic.KVCache(pages), freq)
+    table = torch.arange(pages.shape[0], dtype=torch.int32, device=dev).view(2, -1)
+    calls = []
+    for b in range(2):  # the step of each sequence alone; the same token again at every call
+        X = torch.randn(1, hidden, generator=torch.Generator().manual_seed(b)).to(BF).to(dev)
+        pos = torch.tensor([n - 1], device=dev)
+        slots = table[b, pos // P].long() * P + pos % P
+        lens = torch.tensor([n], dtype=torch.int32, device=dev)
+        calls.append(lambda X=X, pos=pos, slots=slots, t=table[b:b + 1].contiguous(), lens=lens: layer.step(X, pos, slots, t, lens))
+    want = [c().clone() for c in calls]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(c())
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    graphs[1].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[1], want[1])
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = calls[0]()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1]) and torch.equal(eager, want[0])
