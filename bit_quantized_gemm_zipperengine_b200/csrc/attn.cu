@@ -27,8 +27,8 @@
 #include <cfloat>
 #include <climits>
 
+#include "attn.cuh"
 #include "half_mma.cuh"
-#include "ops.cuh"
 
 namespace mq {
 
@@ -36,13 +36,9 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStep = 32;               // tokens a warp takes at a time
 constexpr int kUnit = kStep * kWarps;   // tokens of a unit
 constexpr int kStages = 2;              // steps in flight per warp (a power of two)
 constexpr int kJoin = 4;                // what a second run costs a CTA, in units
-constexpr int kMaxLen = 1 << 30;        // cached tokens of a sequence
-constexpr float kShift = 7.0f;          // exponent offset of the fp16 softmax weights
-constexpr float kSlack = 8.0f;          // how far a score may pass its row's reference
 
 template <int NT>
 constexpr int ctas_per_sm() { return NT == 1 ? 3 : 2; }
@@ -55,42 +51,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// Sequence b: its rows of q and its length, checked.
-struct Seq {
-    int row0, nq, len;
-};
-__device__ __forceinline__ Seq seq_of(const AttnParams& p, int b, bool report) {
-    Seq s;
-    s.row0 = p.cu_q ? __ldg(p.cu_q + b) : b;
-    const int hi = p.cu_q ? __ldg(p.cu_q + b + 1) : b + 1;
-    s.nq = hi - s.row0;
-    s.len = __ldg(p.kv_len + b);
-    if (s.row0 < 0 || hi < s.row0 || hi > p.T) {
-        if (report) report_index(p.err);
-        s.row0 = s.nq = 0;
-    }
-    if (s.len < 0 || s.len > kMaxLen || s.len > (int64_t)p.max_pages * p.cache.page_size) {
-        if (report) report_index(p.err);
-        s.len = 0;
-    }
-    return s;
-}
-// The tokens that rows [r0, r0 + rows) of a sequence's nq * G rows can see: [begin, end), begin
-// rounded down to a step.
-__device__ __forceinline__ void range_of(const Seq& s, const FastDiv& G, int window, int r0, int rows, int& begin, int& end) {
-    const int last = min(r0 + rows, s.nq * G.d) - 1;
-    end = max(0, s.len - s.nq + (int)G.div(last) + 1);
-    begin = 0;
-    if (window > 0) {
-        const int64_t lo = (int64_t)s.len - s.nq + (int)G.div(r0) - window + 1;
-        begin = lo > 0 ? (int)lo / kStep * kStep : 0;
-    }
 }
 __device__ __forceinline__ int units_of(const Seq& s, const FastDiv& G, int window, int r0, int rows) {
     int begin, end;
@@ -123,11 +83,6 @@ __device__ __forceinline__ float warp_max(float v) {
     for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
-// ln of the sum of 2^z, kept as sum = sum of 2^(z - top + kShift).
-__device__ __forceinline__ float lse_of(float top, float sum) {
-    return sum == 0.0f ? -INFINITY : (top - kShift + log2f(sum)) * 0.69314718055994531f;
-}
-
 template <int D, int NT, bool F16>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const AttnParams p) {
     constexpr int R = 8 * NT;           // rows of a tile
@@ -826,6 +781,7 @@ cudaError_t launch_attn(const AttnParams& p0, int D, int max_q, bool f16, cudaSt
     p.by_group = FastDiv(p.q.heads / p.cache.heads);
     p.by_page = FastDiv(p.cache.page_size);
     p.scale *= 1.4426950408889634f;  // scores in powers of two
+    if (attn_rows_serves(p, D)) return launch_attn_rows(p, f16, s);
     const int nt = row_tiles(p.q.heads, p.cache.heads, max_q), grid = grid_of(nt);
     p.by_grid = FastDiv(grid);
     if (D == 64) {

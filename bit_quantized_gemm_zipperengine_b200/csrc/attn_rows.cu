@@ -1,0 +1,428 @@
+// Attention over the NVFP4 cache for many query rows a cache head (prompts): the formula, the
+// masks and the softmax reference of attn.cu, on tcgen05 with tensor-memory accumulators.
+//
+// What bounds it: the products, 4 D flops a row and seen token, and one exponential each (16
+// a clock and SM, as long as the products of D = 128). A tile of 128 query rows (tokens times
+// the query heads that share a cache head) is one operand, so 128 rows share a conversion
+// of the cache, where attn.cu's 24 spend their time converting.
+//
+// A CTA takes a tile; the cached tokens pass in steps of 64. Roles:
+//  - four warps convert: a record (16 tokens) each, codes and scales from global memory, a step
+//    ahead in registers, to exact fp16 in shared memory (128-byte swizzle, two buffers);
+//  - one thread issues S = Q K^T (64 columns of tensor memory, two buffers) and O += P V
+//    (128 columns; V's tokens are rows in memory, so it is the operand with d running fastest);
+//  - four warps hold a query row a thread: the row's maximum and sum need no shuffles. P goes
+//    back over S in fp16 and is read as an operand from there. O is rescaled in place when a
+//    row's reference rises, which the slack of 2^8 makes rare.
+// Two CTAs an SM (256 columns, 97 KB) overlap one's softmax with the other's products.
+#include <cfloat>
+#include <climits>
+
+#include "attn.cuh"
+#include "half_mma.cuh"
+
+namespace mq {
+
+namespace {
+
+constexpr int kD = 128;
+constexpr int kRows = 128;   // query rows of a tile, one softmax thread each
+constexpr int kTile = 64;    // tokens of a step
+constexpr int kConvert = 4;  // first converting warp
+constexpr int kIssue = 8;    // the warp that issues products
+constexpr int kThreads = 32 * (kIssue + 1);
+constexpr int kOffK = kRows * kD * 2, kKv = kTile * kD * 2, kOffV = kOffK + 2 * kKv;
+constexpr int kSmem = kOffV + 2 * kKv;
+constexpr uint32_t kCols = 256, kOutCol = 128;  // tensor memory: S, S, O
+
+// fp16 operands, fp32 accumulator: D format 1 (bits 4-5), A and B format 0, bit 16: B's
+// rows run fastest, N >> 3 in bits 17-22, M >> 4 in bits 24-28.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_rows_fast) {
+    return (1u << 4) | ((b_rows_fast ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// 16 columns of the warp's 32 lanes; complete after tmem_st_wait.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Byte of 16-byte piece c of row n in a [rows][64 elements] block with 128-byte swizzle.
+__device__ __forceinline__ int swizzled(int n, int c) { return n * 128 + ((c ^ (n & 7)) << 4); }
+
+template <bool F16>
+__global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ uint64_t q_full, kv_full[2], s_full[2], p_full[2], done[2];
+    __shared__ uint32_t tmem_at;
+    __shared__ int work[2], lost[2][4];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int H = p.cache.heads;
+    const FastDiv& G = p.by_group;
+    // Tensor memory before the next kernel may start: it could take what is left of it.
+    if (warp == kIssue) {
+        tmem_alloc(&tmem_at, kCols);
+        tmem_relinquish();
+    }
+    if (tid == 0) {
+        mbar_init(&q_full, kRows);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(kv_full + b, 128);
+            mbar_init(s_full + b, 1);
+            mbar_init(p_full + b, kRows);
+            mbar_init(done + b, 1);
+        }
+        work[0] = -1;
+    }
+    mbar_fence_init();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_at;
+    const bool placed = (smem_u32(smem) & 1023u) == 0;  // the swizzle repeats every 1024 bytes
+    griddep_wait();
+    griddep_launch();
+
+    // The CTA's tile: sequences in order, then tiles from the last rows on (they see most), then heads.
+    if (warp == 0) {
+        int64_t base = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const int b = b0 + lane;
+            const Seq s = b < p.B ? seq_of(p, b, blockIdx.x == 0) : Seq{0, 0, 0};
+            const int64_t n = (int64_t)((s.nq * G.d + kRows - 1) / kRows) * H;
+            int64_t x = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            x += base;
+            if (n > 0 && (int64_t)blockIdx.x >= x - n && (int64_t)blockIdx.x < x) {
+                work[0] = b;
+                work[1] = (int)(blockIdx.x - (x - n));
+            }
+            base = __shfl_sync(0xffffffffu, x, 31);
+            if (blockIdx.x != 0 && (int64_t)blockIdx.x < base) break;  // CTA 0 checks every sequence
+        }
+        if (!placed && lane == 0) report_index(p.err);
+    }
+    __syncthreads();
+    if (work[0] >= 0 && placed) {
+        const Seq s = seq_of(p, work[0], false);
+        const int rows = s.nq * G.d, tiles = (rows + kRows - 1) / kRows;
+        const int h = work[1] % H, r0 = (tiles - 1 - work[1] / H) * kRows;
+        int begin, end;
+        range_of(s, G, p.window, r0, kRows, begin, end);
+        const int steps = end > begin ? (end - begin + kTile - 1) / kTile : 0;
+
+        // the warp decides together; after a wait that gave up (reported) its loop ends
+        auto wait = [&](uint64_t* bar, int use) { return __all_sync(0xffffffffu, mbar_wait_err(bar, use & 1, p.err)) != 0; };
+
+        if (warp >= kConvert && warp < kIssue) {
+            // ------------------------------------------------------------ conversion
+            const int r = warp - kConvert, n8 = lane & 7, t = lane >> 3;  // record of a step; token, piece
+            const int lo_min = p.window > 0 ? s.len - s.nq + (int)G.div(r0) + 1 - p.window : 0;
+            auto record = [&](int step) -> const uint8_t* {
+                const int j = begin + step * kTile + 16 * r;
+                if (step >= steps || j >= end) return nullptr;
+                const int pg = (int)p.by_page.div(j);
+                const int page = __ldg(p.table + work[0] * p.table_stride + pg);
+                if (page < 0 || page >= p.cache.num_pages) {
+                    report_index(p.err);
+                    return nullptr;
+                }
+                return p.cache.pages + (((int64_t)page * H + h) * (p.cache.page_size >> 4) + ((j - pg * p.cache.page_size) >> 4)) * (18 * kD);
+            };
+            // a lane's part of a record: keys of tokens n8 and n8 + 8, 32 elements each; values of
+            // both tokens in groups t and t + 4
+            uint4 kc[2];
+            uint2 vc[4];
+            uint32_t ks[2], vs = 0;
+            bool there = false;
+            auto fetch = [&](const uint8_t* rec) {
+                there = rec != nullptr;
+                if (!there) {
+                    kc[0] = kc[1] = make_uint4(0, 0, 0, 0);
+                    vc[0] = vc[1] = vc[2] = vc[3] = make_uint2(0, 0);
+                    ks[0] = ks[1] = vs = 0;
+                    return;
+                }
+                vs = 0;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int i = n8 + 8 * u;
+                    kc[u] = __ldg(reinterpret_cast<const uint4*>(rec + i * (kD / 2) + 16 * t));
+                    ks[u] = __ldg(reinterpret_cast<const uint16_t*>(rec + rec_kscale<kD>(i, 2 * t)));
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        vc[2 * u + w] = __ldg(reinterpret_cast<const uint2*>(rec + rec_vcodes<kD>(i, t + 4 * w)));
+                        vs |= (uint32_t)__ldg(rec + rec_vscale<kD>(i, t + 4 * w)) << (16 * u + 8 * w);
+                    }
+                }
+            };
+            auto put = [&](uint8_t* dst, uint32_t codes, __half2 f) {
+                uint32_t x[4];
+                e2m1x8_half(codes, x);
+                *reinterpret_cast<uint4*>(dst) = make_uint4(mul_h2(x[0], f), mul_h2(x[1], f), mul_h2(x[2], f), mul_h2(x[3], f));
+            };
+            fetch(record(0));
+            const uint8_t* next = record(1);
+            for (int i = 0; i < steps; ++i) {
+                const int b = i & 1, j0 = begin + i * kTile + 16 * r;
+                uint4 k2[2] = {kc[0], kc[1]};
+                uint2 v4[4] = {vc[0], vc[1], vc[2], vc[3]};
+                const uint32_t ks2 = ks[0] | ks[1] << 16;
+                uint32_t vs4 = vs;
+                const bool here = there;
+                fetch(next);
+                next = record(i + 2);
+                // tokens that no row sees may hold anything: their values' scales become zero
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    if (j0 + n8 + 8 * u >= end || j0 + n8 + 8 * u < lo_min) vs4 &= u ? 0x0000FFFFu : 0xFFFF0000u;
+                if (i >= 2 && !wait(done + b, (i >> 1) - 1)) break;
+                uint8_t *K = smem + kOffK + b * kKv, *V = smem + kOffV + b * kKv;
+                uint32_t f[2], g[2];
+                e4m3x4_half(ks2, f[0], f[1]);
+                e4m3x4_half(vs4, g[0], g[1]);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int n = 16 * r + n8 + 8 * u;
+                    uint8_t* at = K + (t >> 1) * (kKv / 2);
+                    const int c = (t & 1) * 4;
+                    put(at + swizzled(n, c), k2[u].x, low2(f[u]));
+                    put(at + swizzled(n, c + 1), k2[u].y, low2(f[u]));
+                    put(at + swizzled(n, c + 2), k2[u].z, high2(f[u]));
+                    put(at + swizzled(n, c + 3), k2[u].w, high2(f[u]));
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {  // group t + 4 w: the w-th 64 elements
+                        put(V + w * (kKv / 2) + swizzled(n, 2 * t), v4[2 * u + w].x, w ? high2(g[u]) : low2(g[u]));
+                        put(V + w * (kKv / 2) + swizzled(n, 2 * t + 1), v4[2 * u + w].y, w ? high2(g[u]) : low2(g[u]));
+                    }
+                }
+                if (lane == 0) lost[b][r] = !here;
+                fence_proxy_async_smem();
+                mbar_arrive(kv_full + b);
+            }
+        } else if (warp == kIssue) {
+            // ------------------------------------------------------------ products
+            constexpr uint32_t iqk = idesc_f16(kRows, kTile, false), ipv = idesc_f16(kRows, kD, true);
+            const uint32_t sq = smem_u32(smem), sk = sq + kOffK, sv = sq + kOffV;
+            auto scores = [&](int b) {
+                if (lane == 0) {
+#pragma unroll
+                    for (int k = 0; k < kD / 16; ++k)
+                        mma_ss(tmem + b * kTile, smem_desc(sq + (k >> 2) * (kOffK / 2) + (k & 3) * 32, 16, 1024, 2),
+                               smem_desc(sk + b * kKv + (k >> 2) * (kKv / 2) + (k & 3) * 32, 16, 1024, 2), iqk, k > 0);
+                    tc_commit(s_full + b);
+                }
+                __syncwarp();
+            };
+            int last = -1;  // the last step whose second product was issued
+            if (steps > 0 && wait(&q_full, 0) && wait(kv_full, 0)) {
+                tc_fence_after();
+                scores(0);
+                for (int i = 0; i < steps; ++i) {
+                    const int b = i & 1;
+                    if (i + 1 < steps) {
+                        // the other S holds the weights of step i - 1 until its product is done
+                        if (i > 0 && !wait(done + (b ^ 1), (i - 1) >> 1)) break;
+                        if (!wait(kv_full + (b ^ 1), (i + 1) >> 1)) break;
+                        tc_fence_after();
+                        scores(b ^ 1);
+                    }
+                    if (!wait(p_full + b, i >> 1)) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+#pragma unroll
+                        for (int k = 0; k < kTile / 16; ++k)
+                            mma_ts(tmem + kOutCol, tmem + b * kTile + 8 * k, smem_desc(sv + b * kKv + k * 2048, kKv / 2, 1024, 2), ipv,
+                                   i > 0 || k > 0);
+                        tc_commit(done + b);
+                    }
+                    __syncwarp();
+                    last = i;
+                }
+                if (last >= 0) wait(done + (last & 1), last >> 1);
+            }
+        } else if (warp < kConvert) {
+            // ------------------------------------------------------------ a query row a thread
+            const int row = r0 + tid;
+            const bool on = row < rows;
+            const int qi = on ? (int)G.div(row) : 0, hq = h * G.d + row - qi * G.d;
+            const int64_t tok = s.row0 + qi;
+            const float gk = p.cache.k_scale ? __ldg(p.cache.k_scale + h) : 1.0f;
+            const float gv = p.cache.v_scale ? __ldg(p.cache.v_scale + h) : 1.0f;
+            float inv = 1.0f;
+            {
+                const uint4* src = reinterpret_cast<const uint4*>(p.q.p + tok * p.q.st + hq * p.q.sh);
+                auto piece = [&](int c) { return on ? __ldg(src + c) : make_uint4(0, 0, 0, 0); };
+                const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;  // the sign of the scale goes into the query: qs > 0
+                float up = 1.0f;
+                if constexpr (!F16) {
+                    uint32_t a = 0;  // the largest element's bits, two at a time
+#pragma unroll 4
+                    for (int c = 0; c < 16; ++c) {
+                        const uint4 v = piece(c);
+                        a = __vmaxu2(a, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+                    }
+                    const uint32_t ex = max(max(a & 0xFFFFu, a >> 16) >> 7, 15u);  // the largest element to [2^14, 2^15)
+                    up = __uint_as_float((268u - ex) << 23);
+                    inv = __uint_as_float((ex - 14u) << 23);
+                }
+#pragma unroll 4
+                for (int c = 0; c < 16; ++c) {
+                    const uint4 v = piece(c);
+                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        if constexpr (!F16) {
+                            const float2 f = widen2<false>(w[x]);
+                            w[x] = narrow2<true>(f.x * up, f.y * up);
+                        }
+                        w[x] ^= flip;
+                    }
+                    *reinterpret_cast<uint4*>(smem + (c >> 3) * (kOffK / 2) + swizzled(tid, c & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&q_full);
+            // never zero: a masked score is -inf before the scale
+            const float qs = fmaxf(inv * gk * fabsf(p.scale), FLT_MIN);
+            const int lim = on ? s.len - s.nq + qi + 1 : INT_MAX;
+            const int lim_first = s.len - s.nq + (int)G.div(r0) + 1;
+            const uint32_t mine = tmem + ((uint32_t)(warp * 32) << 16);  // this warp's lanes
+            float m = -INFINITY, ref = 0.0f, limit = -INFINITY, l = 0.0f;
+            bool alive = true;
+            for (int i = 0; i < steps; ++i) {
+                const int b = i & 1, j0 = begin + i * kTile;
+                alive = wait(s_full + b, i >> 1) && wait(kv_full + b, i >> 1);
+                if (!alive) break;
+                tc_fence_after();
+                float z[kTile];
+                tmem_ld_chunks<kTile / 16>(mine + b * kTile, 0xF, z);
+                const int gone = (lost[b][0] & 1) | (lost[b][1] & 1) << 1 | (lost[b][2] & 1) << 2 | (lost[b][3] & 1) << 3;
+                const bool whole = gone == 0 && j0 + kTile <= min(lim_first, end) && (p.window == 0 || j0 >= end - p.window);
+                if (!whole) {
+                    const int hi = min(lim, end) - j0, lo = p.window > 0 ? lim - p.window - j0 : 0;
+#pragma unroll
+                    for (int c = 0; c < kTile; ++c)
+                        if (c >= hi || c < lo || ((gone >> (c >> 4)) & 1)) z[c] = -INFINITY;
+                }
+                float top = z[0];
+#pragma unroll
+                for (int c = 1; c + 1 < kTile; c += 2) top = max3(top, z[c], z[c + 1]);
+                top = fmaxf(top, z[kTile - 1]);
+                if (__any_sync(0xffffffffu, top > limit)) {
+                    const float mn = fmaxf(m, top * qs);
+                    const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
+                    m = mn;
+                    ref = mn == -INFINITY ? 0.0f : mn - kShift;
+                    limit = (mn + kSlack) / qs;
+                    l *= f;
+                    if (i > 0) {
+                        alive = wait(done + (b ^ 1), (i - 1) >> 1);
+                        if (!alive) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < kD; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16_issue(mine + kOutCol + c, o);
+                            tmem_ld_wait16(o);
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                            tmem_st16(mine + kOutCol + c, o);
+                        }
+                    }
+                }
+                float l2 = 0.0f;
+#pragma unroll
+                for (int c0 = 0; c0 < kTile; c0 += 32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const float x = ex2(__fmaf_rn(z[c0 + 2 * c], qs, -ref)), y = ex2(__fmaf_rn(z[c0 + 2 * c + 1], qs, -ref));
+                        l += x;
+                        l2 += y;
+                        w[c] = narrow2<true>(x, y);
+                    }
+                    tmem_st16(mine + b * kTile + c0 / 2, w);
+                }
+                l += l2;
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(p_full + b);
+            }
+            if (steps > 0 && alive) alive = wait(done + ((steps - 1) & 1), (steps - 1) >> 1);
+            if (alive) {
+                tc_fence_after();
+                const float back = l == 0.0f ? 0.0f : gv / l;
+                uint16_t* dst = p.o.p + tok * p.o.st + hq * p.o.sh;
+#pragma unroll 1
+                for (int c = 0; c < kD; c += 16) {
+                    uint32_t o[16];
+                    if (steps > 0) {
+                        tmem_ld16_issue(mine + kOutCol + c, o);
+                        tmem_ld_wait16(o);
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) o[x] = 0u;
+                    }
+                    uint32_t w[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) w[x] = narrow2<F16>(__uint_as_float(o[2 * x]) * back, __uint_as_float(o[2 * x + 1]) * back);
+                    if (on) {
+                        *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
+                }
+                if (on && p.lse) p.lse[tok * p.q.heads + hq] = lse_of(m, l);
+            }
+            tc_fence_before();
+        }
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kIssue) tmem_dealloc(tmem, kCols);
+}
+
+template <bool F16>
+cudaError_t rows_of(const AttnParams& p, unsigned grid, cudaStream_t s) {
+    static std::atomic<bool> done[64];
+    const cudaError_t e = once_per_device(
+        done, [] { return cudaFuncSetAttribute(k_attn_rows<F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
+    if (e != cudaSuccess) return e;
+    return launch_pdl(k_attn_rows<F16>, dim3(grid), dim3(kThreads), kSmem, s, 1, p);
+}
+
+}  // namespace
+
+bool attn_rows_serves(const AttnParams& p, int D) {
+    const int64_t rows = (int64_t)p.T * (p.q.heads / p.cache.heads);  // of a cache head
+    return D == kD && rows >= (int64_t)kRows * p.B && rows / kRows * p.cache.heads >= device_sms() &&
+           (rows / kRows + p.B) * p.cache.heads < INT_MAX;
+}
+
+cudaError_t launch_attn_rows(const AttnParams& p, bool f16, cudaStream_t s) {
+    const int64_t rows = (int64_t)p.T * (p.q.heads / p.cache.heads);
+    const unsigned grid = (unsigned)((rows / kRows + p.B) * p.cache.heads);  // at most: every sequence ends in a part of a tile
+    return f16 ? rows_of<true>(p, grid, s) : rows_of<false>(p, grid, s);
+}
+
+}  // namespace mq

@@ -415,6 +415,66 @@ def test_attention(case, dtype, dev, mosaic):
         within(o3, want[0], bo, "out, max_q = 1")
 
 
+ROWS = [
+    # many query rows a cache head: lens, query tokens, Hq, H, P, window
+    ([700, 301], [300, 301], 64, 16, 64, 0),
+    ([900, 1], [800, 1], 32, 32, 16, 0),                  # a head of its own for each query head
+    ([256, 9, 40], [256, 0, 77], 80, 16, 48, 50),         # a window; more query tokens than cached
+    ([3000, 64, 64], [200, 64, 65], 96, 16, 128, 0),      # behind a prefix
+    ([640, 700], [128, 600], 64, 16, 32, 129),
+    ([0, 500], [130, 400], 40, 20, 16, 0),                # rows that see nothing
+    ([64, 65, 63, 129], [64, 65, 63, 129], 128, 32, 64, 1),
+]
+
+
+@pytest.mark.parametrize("case", range(len(ROWS)))
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_attention_many_rows(case, dtype, dev, mosaic):
+    lens, nqs, Hq, H, P, window = ROWS[case]
+    q, pages, ks, vs, table, kv_len, cu = attn_inputs(lens, nqs, Hq, H, 128, P, dtype, 70 + case, dev, qmul=1.0 + case)
+    scale = (-1) ** case * 128 ** -0.5
+    want = ref.attention(q, pages, ks, vs, table, lens, nqs, scale, window)
+    o, lse = run_attn(mosaic, q, pages, ks, vs, table, kv_len, cu, max(nqs), scale, window, dtype)
+    bo, bl = attn_bounds(*want, dtype, lens)
+    within(o, want[0], bo, "out")
+    dead = want[1] == -math.inf
+    assert (lse[dead] == -math.inf).all() and (o[dead] == 0).all()
+    within(lse[~dead], want[1][~dead], bl[~dead], "lse")
+    o2, lse2 = run_attn(mosaic, q, pages, ks, vs, table, kv_len, cu, max(nqs), scale, window, dtype)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_attention_many_rows_bad_pages_and_nan(dev, mosaic):
+    """A page that is not there leaves its tokens out, as the same cache without them would; a
+    NaN in a query stays in its row; rows of no sequence stay as they were."""
+    lens, nqs, P = [640, 300], [400, 300], 64
+    q, pages, ks, vs, table, kv_len, cu = attn_inputs(lens, nqs, 64, 16, 128, P, BF, 91, dev)
+    want = ref.attention(q, pages, ks, vs, table, lens, nqs, 0.09, 0)
+    bound = attn_bounds(*want, BF, lens)[0]
+    q = torch.cat((q, q[:3]))
+    q[7, 5, 100] = math.nan
+    hit = torch.zeros(q.shape[:2], dtype=torch.bool, device=dev)
+    hit[7, 5] = True
+    o, lse = run_attn(mosaic, q, pages, ks, vs, table, kv_len, cu, 400, 0.09, 0, BF)
+    assert torch.isnan(o[hit]).all() and torch.isnan(lse[hit]).all() and (o[700:] == 77).all() and (lse[700:] == 77).all()
+    ok = ~hit[:700]
+    within(o[:700][ok], want[0][ok], bound[ok])
+    for bad in (-1, pages.shape[0]):
+        t = table.clone()
+        t[0, 9] = bad  # the last 64 tokens of the first sequence
+        o, lse = run_attn(mosaic, q, pages, ks, vs, t, kv_len, cu, 400, 0.09, 0, BF)
+        assert mosaic.mq_get_error() == 1
+        # rows in front of the page are unchanged; those behind it see what a window of none would
+        within(o[:336][ok[:336]], want[0][:336][ok[:336]], bound[:336][ok[:336]])
+        at576 = ref.attention(q[335:336], pages, ks, vs, table, [576], [1], 0.09, 0)
+        q1 = q.clone()
+        q1[336:400] = q[335]
+        o, _ = run_attn(mosaic, q1, pages, ks, vs, t, kv_len, cu, 400, 0.09, 0, BF)
+        assert mosaic.mq_get_error() == 1
+        within(o[335:400], at576[0].expand(65, -1, -1), attn_bounds(*at576, BF, [576])[0].expand(65, -1, -1))
+        within(o[400:700], want[0][400:], bound[400:], "the other sequence")
+
+
 @pytest.mark.parametrize("qmul,scale", [(60.0, 0.5), (1e-3, 1.0), (1.0, 0.0), (4.0, -0.3)])
 def test_attention_sharp_flat_and_odd_scales(qmul, scale, dev, mosaic):
     lens, nqs = [777, 64, 1], [2, 1, 1]
