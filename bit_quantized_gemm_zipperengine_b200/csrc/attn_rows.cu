@@ -69,9 +69,10 @@ __device__ __forceinline__ int swizzled(int n, int c) { return n * 128 + ((c ^ (
 template <bool F16>
 __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ uint64_t q_full, kv_full[2], s_full[2], p_full[2], done[2];
+    __shared__ uint64_t q_full, k_full[2], v_full[2], s_full[2], p_full[2], done[2];
     __shared__ uint32_t tmem_at;
-    __shared__ int work[2], lost[2][4];
+    __shared__ int work[2];
+    __shared__ volatile int lost[4][4];  // of step i at i % 4: written before its keys, read before step i + 4's keys
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int H = p.cache.heads;
     const FastDiv& G = p.by_group;
@@ -83,7 +84,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
     if (tid == 0) {
         mbar_init(&q_full, kRows);
         for (int b = 0; b < 2; ++b) {
-            mbar_init(kv_full + b, 128);
+            mbar_init(k_full + b, 128);
+            mbar_init(v_full + b, 128);
             mbar_init(s_full + b, 1);
             mbar_init(p_full + b, kRows);
             mbar_init(done + b, 1);
@@ -196,11 +198,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
                     if (j0 + n8 + 8 * u >= end || j0 + n8 + 8 * u < lo_min) vs4 &= u ? 0x0000FFFFu : 0xFFFF0000u;
-                if (i >= 2 && !wait(done + b, (i >> 1) - 1)) break;
+                // the keys' buffer is free when the scores of step i - 2 are there, long before their weights
+                if (i >= 2 && !wait(s_full + b, (i >> 1) - 1)) break;
                 uint8_t *K = smem + kOffK + b * kKv, *V = smem + kOffV + b * kKv;
                 uint32_t f[2], g[2];
                 e4m3x4_half(ks2, f[0], f[1]);
                 e4m3x4_half(vs4, g[0], g[1]);
+                if (lane == 0) lost[i & 3][r] = !here;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int n = 16 * r + n8 + 8 * u;
@@ -210,15 +214,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
                     put(at + swizzled(n, c + 1), k2[u].y, low2(f[u]));
                     put(at + swizzled(n, c + 2), k2[u].z, high2(f[u]));
                     put(at + swizzled(n, c + 3), k2[u].w, high2(f[u]));
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(k_full + b);
+                if (i >= 2 && !wait(done + b, (i >> 1) - 1)) break;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int n = 16 * r + n8 + 8 * u;
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {  // group t + 4 w: the w-th 64 elements
                         put(V + w * (kKv / 2) + swizzled(n, 2 * t), v4[2 * u + w].x, w ? high2(g[u]) : low2(g[u]));
                         put(V + w * (kKv / 2) + swizzled(n, 2 * t + 1), v4[2 * u + w].y, w ? high2(g[u]) : low2(g[u]));
                     }
                 }
-                if (lane == 0) lost[b][r] = !here;
                 fence_proxy_async_smem();
-                mbar_arrive(kv_full + b);
+                mbar_arrive(v_full + b);
             }
         } else if (warp == kIssue) {
             // ------------------------------------------------------------ products
@@ -235,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
                 __syncwarp();
             };
             int last = -1;  // the last step whose second product was issued
-            if (steps > 0 && wait(&q_full, 0) && wait(kv_full, 0)) {
+            if (steps > 0 && wait(&q_full, 0) && wait(k_full, 0)) {
                 tc_fence_after();
                 scores(0);
                 for (int i = 0; i < steps; ++i) {
@@ -243,11 +253,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
                     if (i + 1 < steps) {
                         // the other S holds the weights of step i - 1 until its product is done
                         if (i > 0 && !wait(done + (b ^ 1), (i - 1) >> 1)) break;
-                        if (!wait(kv_full + (b ^ 1), (i + 1) >> 1)) break;
+                        if (!wait(k_full + (b ^ 1), (i + 1) >> 1)) break;
                         tc_fence_after();
                         scores(b ^ 1);
                     }
-                    if (!wait(p_full + b, i >> 1)) break;
+                    if (!wait(v_full + b, i >> 1) || !wait(p_full + b, i >> 1)) break;
                     tc_fence_after();
                     if (lane == 0) {
 #pragma unroll
@@ -312,12 +322,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
             bool alive = true;
             for (int i = 0; i < steps; ++i) {
                 const int b = i & 1, j0 = begin + i * kTile;
-                alive = wait(s_full + b, i >> 1) && wait(kv_full + b, i >> 1);
+                alive = wait(s_full + b, i >> 1);
                 if (!alive) break;
                 tc_fence_after();
                 float z[kTile];
                 tmem_ld_chunks<kTile / 16>(mine + b * kTile, 0xF, z);
-                const int gone = (lost[b][0] & 1) | (lost[b][1] & 1) << 1 | (lost[b][2] & 1) << 2 | (lost[b][3] & 1) << 3;
+                const volatile int* no = lost[i & 3];
+                const int gone = no[0] | no[1] << 1 | no[2] << 2 | no[3] << 3;
                 const bool whole = gone == 0 && j0 + kTile <= min(lim_first, end) && (p.window == 0 || j0 >= end - p.window);
                 if (!whole) {
                     const int hi = min(lim, end) - j0, lo = p.window > 0 ? lim - p.window - j0 : 0;
