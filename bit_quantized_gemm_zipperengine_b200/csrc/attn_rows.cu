@@ -63,6 +63,28 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+__device__ __forceinline__ float2 parts_of(uint64_t v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+    uint64_t v;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+
 // Byte of 16-byte piece c of row n in a [rows][64 elements] block with 128-byte swizzle.
 __device__ __forceinline__ int swizzled(int n, int c) { return n * 128 + ((c ^ (n & 7)) << 4); }
 
@@ -336,10 +358,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
                     for (int c = 0; c < kTile; ++c)
                         if (c >= hi || c < lo || ((gone >> (c >> 4)) & 1)) z[c] = -INFINITY;
                 }
-                float top = z[0];
+                float tops[4];
 #pragma unroll
-                for (int c = 1; c + 1 < kTile; c += 2) top = max3(top, z[c], z[c + 1]);
-                top = fmaxf(top, z[kTile - 1]);
+                for (int x = 0; x < 4; ++x) {
+                    tops[x] = fmaxf(z[16 * x], z[16 * x + 1]);
+#pragma unroll
+                    for (int c = 2; c < 16; c += 2) tops[x] = max3(tops[x], z[16 * x + c], z[16 * x + c + 1]);
+                }
+                const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
                 if (__any_sync(0xffffffffu, top > limit)) {
                     const float mn = fmaxf(m, top * qs);
                     const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
@@ -362,20 +388,22 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
                         }
                     }
                 }
-                float l2 = 0.0f;
+                const uint64_t q2 = pair_of(qs, qs), r2 = pair_of(-ref, -ref);
+                uint64_t sum[2] = {0, 0};
 #pragma unroll
                 for (int c0 = 0; c0 < kTile; c0 += 32) {
                     uint32_t w[16];
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
-                        const float x = ex2(__fmaf_rn(z[c0 + 2 * c], qs, -ref)), y = ex2(__fmaf_rn(z[c0 + 2 * c + 1], qs, -ref));
-                        l += x;
-                        l2 += y;
+                        const float2 e = parts_of(fma_pair(pair_of(z[c0 + 2 * c], z[c0 + 2 * c + 1]), q2, r2));
+                        const float x = ex2(e.x), y = ex2(e.y);
+                        sum[c & 1] = add_pair(sum[c & 1], pair_of(x, y));
                         w[c] = narrow2<true>(x, y);
                     }
                     tmem_st16(mine + b * kTile + c0 / 2, w);
                 }
-                l += l2;
+                const float2 both = parts_of(add_pair(sum[0], sum[1]));
+                l += both.x + both.y;
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(p_full + b);
