@@ -9,10 +9,10 @@
 // A CTA takes a tile; the cached tokens pass in steps of 64. Roles:
 //  - four warps convert: a record (16 tokens) each, codes and scales from global memory, a step
 //    ahead in registers, to exact fp16 in shared memory (128-byte swizzle, two buffers);
-//  - one thread issues S = Q K^T (64 columns of tensor memory, two buffers) and O += P V
-//    (128 columns; V's tokens are rows in memory, so it is the operand with d running fastest);
-//  - four warps hold a query row a thread: the row's maximum and sum need no shuffles. P goes
-//    back over S in fp16 and is read as an operand from there. O is rescaled in place when a
+//  - one thread (elected by its warp: the compiler serialises what a lane test guards) issues S = Q K^T (64 columns of tensor memory) and O += P V (128 columns; V's tokens are rows in memory, so it is the operand with d running fastest);
+//  - four warps hold a query row a thread: the row's maximum and sum need no shuffles. S is free
+//    for the next step's scores as soon as it is in registers; P goes back in fp16 (two buffers
+//    of 32 columns) and is read as an operand from there. O is rescaled in place when a
 //    row's reference rises, which the slack of 2^8 makes rare.
 // Two CTAs an SM (256 columns, 97 KB) overlap one's softmax with the other's products.
 #include <cfloat>
@@ -33,7 +33,7 @@ constexpr int kIssue = 8;    // the warp that issues products
 constexpr int kThreads = 32 * (kIssue + 1);
 constexpr int kOffK = kRows * kD * 2, kKv = kTile * kD * 2, kOffV = kOffK + 2 * kKv;
 constexpr int kSmem = kOffV + 2 * kKv;
-constexpr uint32_t kCols = 256, kOutCol = 128;  // tensor memory: S, S, O
+constexpr uint32_t kCols = 256, kWeightCol = 64, kOutCol = 128;  // tensor memory: S, P, P, O
 
 // fp16 operands, fp32 accumulator: D format 1 (bits 4-5), A and B format 0, bit 16: B's
 // rows run fastest, N >> 3 in bits 17-22, M >> 4 in bits 24-28.
@@ -91,7 +91,7 @@ __device__ __forceinline__ int swizzled(int n, int c) { return n * 128 + ((c ^ (
 template <bool F16>
 __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ uint64_t q_full, k_full[2], v_full[2], s_full[2], p_full[2], done[2];
+    __shared__ uint64_t q_full, k_full[2], v_full[2], s_full[2], s_free, p_full[2], done[2];
     __shared__ uint32_t tmem_at;
     __shared__ int work[2];
     __shared__ volatile int lost[4][4];  // of step i at i % 4: written before its keys, read before step i + 4's keys
@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
     }
     if (tid == 0) {
         mbar_init(&q_full, kRows);
+        mbar_init(&s_free, kRows);
         for (int b = 0; b < 2; ++b) {
             mbar_init(k_full + b, 128);
             mbar_init(v_full + b, 128);
@@ -177,17 +178,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
             // both tokens in groups t and t + 4
             uint4 kc[2];
             uint2 vc[4];
-            uint32_t ks[2], vs = 0;
+            uint32_t ks[2], vs[4];
             bool there = false;
             auto fetch = [&](const uint8_t* rec) {
                 there = rec != nullptr;
                 if (!there) {
                     kc[0] = kc[1] = make_uint4(0, 0, 0, 0);
                     vc[0] = vc[1] = vc[2] = vc[3] = make_uint2(0, 0);
-                    ks[0] = ks[1] = vs = 0;
+                    ks[0] = ks[1] = vs[0] = vs[1] = vs[2] = vs[3] = 0;
                     return;
                 }
-                vs = 0;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int i = n8 + 8 * u;
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
                         vc[2 * u + w] = __ldg(reinterpret_cast<const uint2*>(rec + rec_vcodes<kD>(i, t + 4 * w)));
-                        vs |= (uint32_t)__ldg(rec + rec_vscale<kD>(i, t + 4 * w)) << (16 * u + 8 * w);
+                        vs[2 * u + w] = __ldg(rec + rec_vscale<kD>(i, t + 4 * w));
                     }
                 }
             };
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
                 uint4 k2[2] = {kc[0], kc[1]};
                 uint2 v4[4] = {vc[0], vc[1], vc[2], vc[3]};
                 const uint32_t ks2 = ks[0] | ks[1] << 16;
-                uint32_t vs4 = vs;
+                uint32_t vs4 = vs[0] | vs[1] << 8 | vs[2] << 16 | vs[3] << 24;
                 const bool here = there;
                 fetch(next);
                 next = record(i + 2);
@@ -257,10 +257,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
             constexpr uint32_t iqk = idesc_f16(kRows, kTile, false), ipv = idesc_f16(kRows, kD, true);
             const uint32_t sq = smem_u32(smem), sk = sq + kOffK, sv = sq + kOffV;
             auto scores = [&](int b) {
-                if (lane == 0) {
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kD / 16; ++k)
-                        mma_ss(tmem + b * kTile, smem_desc(sq + (k >> 2) * (kOffK / 2) + (k & 3) * 32, 16, 1024, 2),
+                        mma_ss(tmem, smem_desc(sq + (k >> 2) * (kOffK / 2) + (k & 3) * 32, 16, 1024, 2),
                                smem_desc(sk + b * kKv + (k >> 2) * (kKv / 2) + (k & 3) * 32, 16, 1024, 2), iqk, k > 0);
                     tc_commit(s_full + b);
                 }
@@ -273,18 +273,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
                 for (int i = 0; i < steps; ++i) {
                     const int b = i & 1;
                     if (i + 1 < steps) {
-                        // the other S holds the weights of step i - 1 until its product is done
-                        if (i > 0 && !wait(done + (b ^ 1), (i - 1) >> 1)) break;
-                        if (!wait(k_full + (b ^ 1), (i + 1) >> 1)) break;
+                        if (!wait(&s_free, i) || !wait(k_full + (b ^ 1), (i + 1) >> 1)) break;
                         tc_fence_after();
                         scores(b ^ 1);
                     }
                     if (!wait(v_full + b, i >> 1) || !wait(p_full + b, i >> 1)) break;
                     tc_fence_after();
-                    if (lane == 0) {
+                    if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < kTile / 16; ++k)
-                            mma_ts(tmem + kOutCol, tmem + b * kTile + 8 * k, smem_desc(sv + b * kKv + k * 2048, kKv / 2, 1024, 2), ipv,
+                            mma_ts(tmem + kOutCol, tmem + kWeightCol + b * (kTile / 2) + 8 * k, smem_desc(sv + b * kKv + k * 2048, kKv / 2, 1024, 2), ipv,
                                    i > 0 || k > 0);
                         tc_commit(done + b);
                     }
@@ -348,7 +346,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
                 if (!alive) break;
                 tc_fence_after();
                 float z[kTile];
-                tmem_ld_chunks<kTile / 16>(mine + b * kTile, 0xF, z);
+                tmem_ld_chunks<kTile / 16>(mine, 0xF, z);
+                tc_fence_before();
+                mbar_arrive(&s_free);
                 const volatile int* no = lost[i & 3];
                 const int gone = no[0] | no[1] << 1 | no[2] << 2 | no[3] << 3;
                 const bool whole = gone == 0 && j0 + kTile <= min(lim_first, end) && (p.window == 0 || j0 >= end - p.window);
@@ -388,6 +388,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
                         }
                     }
                 }
+                if (i >= 2 && !(alive = wait(done + b, (i >> 1) - 1))) break;
+                tc_fence_after();
                 const uint64_t q2 = pair_of(qs, qs), r2 = pair_of(-ref, -ref);
                 uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -400,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
                         sum[c & 1] = add_pair(sum[c & 1], pair_of(x, y));
                         w[c] = narrow2<true>(x, y);
                     }
-                    tmem_st16(mine + b * kTile + c0 / 2, w);
+                    tmem_st16(mine + kWeightCol + b * (kTile / 2) + c0 / 2, w);
                 }
                 const float2 both = parts_of(add_pair(sum[0], sum[1]));
                 l += both.x + both.y;

@@ -70,17 +70,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
     }
 }
 
-// One lane of a converged warp (the same lane every time the full warp calls it).
-__device__ __forceinline__ bool elect_one() {
-    uint32_t pred;
-    asm volatile(
-        "{\n\t.reg .pred P;\n\t.reg .b32 r;\n\t"
-        "elect.sync r|P, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, P;\n\t}"
-        : "=r"(pred));
-    return pred != 0;
-}
-
 // Bounded wait by a whole warp: all lanes poll, and leave together with lane 0's verdict.
 // Role loops (producer, MMA issuer) run converged and let one elected lane issue:
 // a loop run by a single lane of an otherwise waiting warp issues far more slowly.
