@@ -26,14 +26,16 @@ namespace mq {
 namespace {
 
 constexpr int kD = 128;
-constexpr int kRows = 128;   // query rows of a tile, one softmax thread each
+constexpr int kRows = 128;   // query rows of an operand, one softmax thread each
+constexpr int kGroups = 2;   // operands of a CTA
+constexpr int kBlock = kGroups * kRows;
 constexpr int kTile = 64;    // tokens of a step
-constexpr int kConvert = 4;  // first converting warp
-constexpr int kIssue = 8;    // the warp that issues products
-constexpr int kThreads = 32 * (kIssue + 1);
-constexpr int kOffK = kRows * kD * 2, kKv = kTile * kD * 2, kOffV = kOffK + 2 * kKv;
+// Warps: one a group that issues its products, four that convert, four a group for the query rows.
+constexpr int kConvert = kGroups, kSoftmax = kConvert + 4;
+constexpr int kThreads = 32 * (kSoftmax + 4 * kGroups);
+constexpr int kQ = kRows * kD * 2, kOffK = kGroups * kQ, kKv = kTile * kD * 2, kOffV = kOffK + 2 * kKv;
 constexpr int kSmem = kOffV + 2 * kKv;
-constexpr uint32_t kCols = 256, kWeightCol = 64, kOutCol = 128;  // tensor memory: S, P, P, O
+constexpr uint32_t kCols = 256, kWeightCol = 64, kOutCol = 128;  // tensor memory of a group: S, P, P, O
 
 // fp16 operands, fp32 accumulator: D format 1 (bits 4-5), A and B format 0, bit 16: B's
 // rows run fastest, N >> 3 in bits 17-22, M >> 4 in bits 24-28.
@@ -89,9 +91,10 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
 __device__ __forceinline__ int swizzled(int n, int c) { return n * 128 + ((c ^ (n & 7)) << 4); }
 
 template <bool F16>
-__global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
+__global__ void __launch_bounds__(kThreads, 1) k_attn_rows(const AttnParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ uint64_t q_full, k_full[2], v_full[2], s_full[2], s_free, p_full[2], done[2];
+    __shared__ uint64_t q_full[kGroups], k_full[2], v_full[2];
+    __shared__ uint64_t s_full[kGroups][2], s_free[kGroups], p_full[kGroups][2], done[kGroups][2];
     __shared__ uint32_t tmem_at;
     __shared__ int work[2];
     __shared__ volatile int lost[4][4];  // of step i at i % 4: written before its keys, read before step i + 4's keys
@@ -99,19 +102,23 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
     const int H = p.cache.heads;
     const FastDiv& G = p.by_group;
     // Tensor memory before the next kernel may start: it could take what is left of it.
-    if (warp == kIssue) {
-        tmem_alloc(&tmem_at, kCols);
+    if (warp == 0) {
+        tmem_alloc(&tmem_at, kGroups * kCols);
         tmem_relinquish();
     }
     if (tid == 0) {
-        mbar_init(&q_full, kRows);
-        mbar_init(&s_free, kRows);
         for (int b = 0; b < 2; ++b) {
             mbar_init(k_full + b, 128);
             mbar_init(v_full + b, 128);
-            mbar_init(s_full + b, 1);
-            mbar_init(p_full + b, kRows);
-            mbar_init(done + b, 1);
+        }
+        for (int g = 0; g < kGroups; ++g) {
+            mbar_init(q_full + g, kRows);
+            mbar_init(s_free + g, kRows);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&s_full[g][b], 1);
+                mbar_init(&p_full[g][b], kRows);
+                mbar_init(&done[g][b], 1);
+            }
         }
         work[0] = -1;
     }
@@ -130,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             const int b = b0 + lane;
             const Seq s = b < p.B ? seq_of(p, b, blockIdx.x == 0) : Seq{0, 0, 0};
-            const int64_t n = (int64_t)((s.nq * G.d + kRows - 1) / kRows) * H;
+            const int64_t n = (int64_t)((s.nq * G.d + kBlock - 1) / kBlock) * H;
             int64_t x = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -150,29 +157,35 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
     __syncthreads();
     if (work[0] >= 0 && placed) {
         const Seq s = seq_of(p, work[0], false);
-        const int rows = s.nq * G.d, tiles = (rows + kRows - 1) / kRows;
-        const int h = work[1] % H, r0 = (tiles - 1 - work[1] / H) * kRows;
+        const int rows = s.nq * G.d, tiles = (rows + kBlock - 1) / kBlock;
+        const int h = work[1] % H, r0 = (tiles - 1 - work[1] / H) * kBlock;
+        const int groups = rows - r0 > kRows ? kGroups : 1;  // the last tile may be short
         int begin, end;
-        range_of(s, G, p.window, r0, kRows, begin, end);
+        range_of(s, G, p.window, r0, kBlock, begin, end);
         const int steps = end > begin ? (end - begin + kTile - 1) / kTile : 0;
 
         // the warp decides together; after a wait that gave up (reported) its loop ends
         auto wait = [&](uint64_t* bar, int use) { return __all_sync(0xffffffffu, mbar_wait_err(bar, use & 1, p.err)) != 0; };
 
-        if (warp >= kConvert && warp < kIssue) {
+        if (warp >= kConvert && warp < kSoftmax) {
             // ------------------------------------------------------------ conversion
             const int r = warp - kConvert, n8 = lane & 7, t = lane >> 3;  // record of a step; token, piece
             const int lo_min = p.window > 0 ? s.len - s.nq + (int)G.div(r0) + 1 - p.window : 0;
-            auto record = [&](int step) -> const uint8_t* {
+            const int32_t* table = p.table + work[0] * p.table_stride;
+            // a step's page number (looked at a step later, when it has arrived), and its record
+            auto page_of = [&](int step) {
+                const int j = begin + step * kTile + 16 * r;
+                return step < steps && j < end ? __ldg(table + p.by_page.div(j)) : 0;
+            };
+            auto record = [&](int step, int page) -> const uint8_t* {
                 const int j = begin + step * kTile + 16 * r;
                 if (step >= steps || j >= end) return nullptr;
-                const int pg = (int)p.by_page.div(j);
-                const int page = __ldg(p.table + work[0] * p.table_stride + pg);
                 if (page < 0 || page >= p.cache.num_pages) {
                     report_index(p.err);
                     return nullptr;
                 }
-                return p.cache.pages + (((int64_t)page * H + h) * (p.cache.page_size >> 4) + ((j - pg * p.cache.page_size) >> 4)) * (18 * kD);
+                const int in = j - (int)p.by_page.div(j) * p.cache.page_size;
+                return p.cache.pages + (((int64_t)page * H + h) * (p.cache.page_size >> 4) + (in >> 4)) * (18 * kD);
             };
             // a lane's part of a record: keys of tokens n8 and n8 + 8, 32 elements each; values of
             // both tokens in groups t and t + 4
@@ -205,8 +218,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
                 e2m1x8_half(codes, x);
                 *reinterpret_cast<uint4*>(dst) = make_uint4(mul_h2(x[0], f), mul_h2(x[1], f), mul_h2(x[2], f), mul_h2(x[3], f));
             };
-            fetch(record(0));
-            const uint8_t* next = record(1);
+            fetch(record(0, page_of(0)));
+            int next = page_of(1);
             for (int i = 0; i < steps; ++i) {
                 const int b = i & 1, j0 = begin + i * kTile + 16 * r;
                 uint4 k2[2] = {kc[0], kc[1]};
@@ -214,14 +227,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
                 const uint32_t ks2 = ks[0] | ks[1] << 16;
                 uint32_t vs4 = vs[0] | vs[1] << 8 | vs[2] << 16 | vs[3] << 24;
                 const bool here = there;
-                fetch(next);
-                next = record(i + 2);
+                fetch(record(i + 1, next));
+                next = page_of(i + 2);
                 // tokens that no row sees may hold anything: their values' scales become zero
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
                     if (j0 + n8 + 8 * u >= end || j0 + n8 + 8 * u < lo_min) vs4 &= u ? 0x0000FFFFu : 0xFFFF0000u;
                 // the keys' buffer is free when the scores of step i - 2 are there, long before their weights
-                if (i >= 2 && !wait(s_full + b, (i >> 1) - 1)) break;
+                if (i >= 2 && !(wait(&s_full[0][b], (i >> 1) - 1) && (groups == 1 || wait(&s_full[1][b], (i >> 1) - 1)))) break;
                 uint8_t *K = smem + kOffK + b * kKv, *V = smem + kOffV + b * kKv;
                 uint32_t f[2], g[2];
                 e4m3x4_half(ks2, f[0], f[1]);
@@ -239,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(k_full + b);
-                if (i >= 2 && !wait(done + b, (i >> 1) - 1)) break;
+                if (i >= 2 && !(wait(&done[0][b], (i >> 1) - 1) && (groups == 1 || wait(&done[1][b], (i >> 1) - 1)))) break;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int n = 16 * r + n8 + 8 * u;
@@ -252,48 +265,49 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
                 fence_proxy_async_smem();
                 mbar_arrive(v_full + b);
             }
-        } else if (warp == kIssue) {
-            // ------------------------------------------------------------ products
+        } else if (warp < groups) {
+            // ------------------------------------------------------------ a group's products
             constexpr uint32_t iqk = idesc_f16(kRows, kTile, false), ipv = idesc_f16(kRows, kD, true);
-            const uint32_t sq = smem_u32(smem), sk = sq + kOffK, sv = sq + kOffV;
+            const int g = warp;
+            const uint32_t sk = smem_u32(smem) + kOffK, sv = smem_u32(smem) + kOffV, sq = smem_u32(smem) + g * kQ, mine = tmem + g * kCols;
             auto scores = [&](int b) {
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kD / 16; ++k)
-                        mma_ss(tmem, smem_desc(sq + (k >> 2) * (kOffK / 2) + (k & 3) * 32, 16, 1024, 2),
+                        mma_ss(mine, smem_desc(sq + (k >> 2) * (kQ / 2) + (k & 3) * 32, 16, 1024, 2),
                                smem_desc(sk + b * kKv + (k >> 2) * (kKv / 2) + (k & 3) * 32, 16, 1024, 2), iqk, k > 0);
-                    tc_commit(s_full + b);
+                    tc_commit(&s_full[g][b]);
                 }
                 __syncwarp();
             };
             int last = -1;  // the last step whose second product was issued
-            if (steps > 0 && wait(&q_full, 0) && wait(k_full, 0)) {
+            if (steps > 0 && wait(k_full, 0) && wait(q_full + g, 0)) {
                 tc_fence_after();
                 scores(0);
                 for (int i = 0; i < steps; ++i) {
                     const int b = i & 1;
-                    if (i + 1 < steps) {
-                        if (!wait(&s_free, i) || !wait(k_full + (b ^ 1), (i + 1) >> 1)) break;
+                    if (i + 1 < steps) {  // the next scores run beside this step's softmax
+                        if (!wait(k_full + (b ^ 1), (i + 1) >> 1) || !wait(s_free + g, i)) break;
                         tc_fence_after();
                         scores(b ^ 1);
                     }
-                    if (!wait(v_full + b, i >> 1) || !wait(p_full + b, i >> 1)) break;
+                    if (!wait(v_full + b, i >> 1) || !wait(&p_full[g][b], i >> 1)) break;
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < kTile / 16; ++k)
-                            mma_ts(tmem + kOutCol, tmem + kWeightCol + b * (kTile / 2) + 8 * k, smem_desc(sv + b * kKv + k * 2048, kKv / 2, 1024, 2), ipv,
-                                   i > 0 || k > 0);
-                        tc_commit(done + b);
+                            mma_ts(mine + kOutCol, mine + kWeightCol + b * (kTile / 2) + 8 * k,
+                                   smem_desc(sv + b * kKv + k * 2048, kKv / 2, 1024, 2), ipv, i > 0 || k > 0);
+                        tc_commit(&done[g][b]);
                     }
                     __syncwarp();
                     last = i;
                 }
-                if (last >= 0) wait(done + (last & 1), last >> 1);
+                if (last >= 0) wait(&done[g][last & 1], last >> 1);
             }
-        } else if (warp < kConvert) {
+        } else if (warp >= kSoftmax && warp < kSoftmax + 4 * groups) {
             // ------------------------------------------------------------ a query row a thread
-            const int row = r0 + tid;
+            const int g = (warp - kSoftmax) >> 2, in = 32 * (warp & 3) + lane, row = r0 + g * kRows + in;
             const bool on = row < rows;
             const int qi = on ? (int)G.div(row) : 0, hq = h * G.d + row - qi * G.d;
             const int64_t tok = s.row0 + qi;
@@ -328,27 +342,27 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
                         }
                         w[x] ^= flip;
                     }
-                    *reinterpret_cast<uint4*>(smem + (c >> 3) * (kOffK / 2) + swizzled(tid, c & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(smem + g * kQ + (c >> 3) * (kQ / 2) + swizzled(in, c & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
             fence_proxy_async_smem();
-            mbar_arrive(&q_full);
+            mbar_arrive(q_full + g);
             // never zero: a masked score is -inf before the scale
             const float qs = fmaxf(inv * gk * fabsf(p.scale), FLT_MIN);
             const int lim = on ? s.len - s.nq + qi + 1 : INT_MAX;
             const int lim_first = s.len - s.nq + (int)G.div(r0) + 1;
-            const uint32_t mine = tmem + ((uint32_t)(warp * 32) << 16);  // this warp's lanes
+            const uint32_t mine = tmem + g * kCols + ((uint32_t)((warp & 3) * 32) << 16);  // this warp's lanes
             float m = -INFINITY, ref = 0.0f, limit = -INFINITY, l = 0.0f;
             bool alive = true;
             for (int i = 0; i < steps; ++i) {
                 const int b = i & 1, j0 = begin + i * kTile;
-                alive = wait(s_full + b, i >> 1);
+                alive = wait(&s_full[g][b], i >> 1);
                 if (!alive) break;
                 tc_fence_after();
                 float z[kTile];
                 tmem_ld_chunks<kTile / 16>(mine, 0xF, z);
                 tc_fence_before();
-                mbar_arrive(&s_free);
+                mbar_arrive(s_free + g);
                 const volatile int* no = lost[i & 3];
                 const int gone = no[0] | no[1] << 1 | no[2] << 2 | no[3] << 3;
                 const bool whole = gone == 0 && j0 + kTile <= min(lim_first, end) && (p.window == 0 || j0 >= end - p.window);
@@ -374,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
                     limit = (mn + kSlack) / qs;
                     l *= f;
                     if (i > 0) {
-                        alive = wait(done + (b ^ 1), (i - 1) >> 1);
+                        alive = wait(&done[g][b ^ 1], (i - 1) >> 1);
                         if (!alive) break;
                         tc_fence_after();
 #pragma unroll 1
@@ -388,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
                         }
                     }
                 }
-                if (i >= 2 && !(alive = wait(done + b, (i >> 1) - 1))) break;
+                if (i >= 2 && !(alive = wait(&done[g][b], (i >> 1) - 1))) break;
                 tc_fence_after();
                 const uint64_t q2 = pair_of(qs, qs), r2 = pair_of(-ref, -ref);
                 uint64_t sum[2] = {0, 0};
@@ -408,9 +422,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
                 l += both.x + both.y;
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(p_full + b);
+                mbar_arrive(&p_full[g][b]);
             }
-            if (steps > 0 && alive) alive = wait(done + ((steps - 1) & 1), (steps - 1) >> 1);
+            if (steps > 0 && alive) alive = wait(&done[g][(steps - 1) & 1], (steps - 1) >> 1);
             if (alive) {
                 tc_fence_after();
                 const float back = l == 0.0f ? 0.0f : gv / l;
@@ -440,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_rows(const AttnParams p) {
     }
     __syncthreads();
     tc_fence_after();
-    if (warp == kIssue) tmem_dealloc(tmem, kCols);
+    if (warp == 0) tmem_dealloc(tmem, kGroups * kCols);
 }
 
 template <bool F16>
@@ -457,12 +471,12 @@ cudaError_t rows_of(const AttnParams& p, unsigned grid, cudaStream_t s) {
 bool attn_rows_serves(const AttnParams& p, int D) {
     const int64_t rows = (int64_t)p.T * (p.q.heads / p.cache.heads);  // of a cache head
     return D == kD && rows >= (int64_t)kRows * p.B && rows / kRows * p.cache.heads >= device_sms() &&
-           (rows / kRows + p.B) * p.cache.heads < INT_MAX;
+           (rows / kBlock + p.B) * p.cache.heads < INT_MAX;
 }
 
 cudaError_t launch_attn_rows(const AttnParams& p, bool f16, cudaStream_t s) {
     const int64_t rows = (int64_t)p.T * (p.q.heads / p.cache.heads);
-    const unsigned grid = (unsigned)((rows / kRows + p.B) * p.cache.heads);  // at most: every sequence ends in a part of a tile
+    const unsigned grid = (unsigned)((rows / kBlock + p.B) * p.cache.heads);  // at most: every sequence ends in a part of a tile
     return f16 ? rows_of<true>(p, grid, s) : rows_of<false>(p, grid, s);
 }
 
