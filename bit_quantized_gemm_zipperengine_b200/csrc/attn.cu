@@ -3,6 +3,11 @@
 //
 // What bounds it: the cache's bytes, 9/8 D a token and head, read once for all the query
 // rows of a cache head (a "row" is a query token and one of the query heads that share it).
+// Calls with many rows a cache head go to attn_rows.cu.
+//
+// Once a long cache streams, the conversions, multiplies and products that share the issue slots
+// are the longer half: 4 x 131072 tokens, 64/8 heads take 127 us (4.8 TB/s), the copies alone
+// 104, the arithmetic alone 122. One sequence of 509 tokens takes 9.8 us, all latency.
 //
 // One pass. A warp takes 32 tokens at a time: two records of the cache, one bulk copy each,
 // into its own ring in shared memory. Its products run on the tensor cores with the
@@ -105,9 +110,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
     griddep_launch();
 
     // The CTA's work. CTA w takes the w-th equal share of all units, in order; or, with fewer
-    // runs than CTAs, every run is cut into equal pieces of at most q units, one CTA each. Then no CTA joins two runs, which costs it about as
-    // much as kJoin units (16 sequences of up to 8192 tokens: 33.2 us by shares, 31.8 by pieces;
-    // 4 of 131072, where pieces waste 5 of 74 units: 126.6 and 132.7).
+    // runs than CTAs, every run is cut into equal pieces of at most q units, one CTA each. Then no
+    // CTA joins two runs, which costs it about as much as kJoin units (16 sequences of up to
+    // 8192 tokens: 33.2 us by shares, 31.8 by pieces; 4 of 131072, where pieces waste 5 of 74
+    // units: 126.6 and 132.7).
     const Seq own = tid < p.B ? seq_of(p, tid, blockIdx.x == 0) : Seq{0, 0, 0};
     const int64_t own_units = seq_units(own, G, p.window, R) * H;
     int64_t mine = own_units, rmine = (int64_t)((own.nq * G.d + R - 1) / R) * H;
@@ -757,8 +763,7 @@ cudaError_t attn_of(const AttnParams& p, int grid, cudaStream_t s) {
 
 // Eights of query rows that a CTA holds. More rows share a step's conversions, up to what the
 // registers hold; with few rows the shorter step wins (8 sequences of up to 4001 tokens and 24
-// rows: 26.4 us by 16, 29.0 by 24; 512 rows: 157 and 143 us; 2 x 2048 rows behind 8192
-// tokens: 661 and 598 us).
+// rows: 26.4 us by 16, 29.0 by 24; 512 rows: 157 and 143 us).
 int row_tiles(int q_heads, int kv_heads, int max_q) {
     const int64_t rows = (int64_t)(q_heads / kv_heads) * max_q;
     return rows <= 8 ? 1 : rows <= 32 ? 2 : 3;

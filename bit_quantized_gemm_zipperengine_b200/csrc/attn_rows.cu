@@ -2,19 +2,26 @@
 // masks and the softmax reference of attn.cu, on tcgen05 with tensor-memory accumulators.
 //
 // What bounds it: the products, 4 D flops a row and seen token, and one exponential each (16
-// a clock and SM, as long as the products of D = 128). A tile of 128 query rows (tokens times
-// the query heads that share a cache head) is one operand, so 128 rows share a conversion
-// of the cache, where attn.cu's 24 spend their time converting.
+// a clock and SM, as long as the products of D = 128). 256 query rows (tokens times the
+// query heads that share a cache head) share a conversion of the cache, where attn.cu's 24
+// spend their time converting: 512 tokens of two sequences behind 8192, 32/8 heads: 162 us, 820
+// TFLOP/s, against 599; a prompt of 4096: 178 against 1508 us.
 //
-// A CTA takes a tile; the cached tokens pass in steps of 64. Roles:
+// A CTA takes a tile of 256 rows, two operands of 128; the cached tokens pass in steps of 64:
 //  - four warps convert: a record (16 tokens) each, codes and scales from global memory, a step
 //    ahead in registers, to exact fp16 in shared memory (128-byte swizzle, two buffers);
-//  - one thread (elected by its warp: the compiler serialises what a lane test guards) issues S = Q K^T (64 columns of tensor memory) and O += P V (128 columns; V's tokens are rows in memory, so it is the operand with d running fastest);
-//  - four warps hold a query row a thread: the row's maximum and sum need no shuffles. S is free
-//    for the next step's scores as soon as it is in registers; P goes back in fp16 (two buffers
-//    of 32 columns) and is read as an operand from there. O is rescaled in place when a
+//  - a warp for each operand issues its products from an elected lane: S = Q K^T (64 columns
+//    of tensor memory) and O += P V (128 columns; V's tokens are rows in memory, so it is the
+//    operand whose rows run fastest). One warp for both took 217 us: its waits and issues, a
+//    hundred cycles each, were the longest chain of a step;
+//  - four warps an operand hold a query row a thread: its maximum and sum need no shuffles. S is
+//    free for the next step's scores as soon as it is in registers; P goes back in fp16 (two
+//    buffers of 32 columns) and is read as an operand from there. O is rescaled in place when a
 //    row's reference rises, which the slack of 2^8 makes rare.
-// Two CTAs an SM (256 columns, 97 KB) overlap one's softmax with the other's products.
+// One such CTA fills an SM (512 columns of tensor memory, 128 KB). Two of 128 rows an SM took
+// 190 us: every step was converted twice. What is left: a step takes 2400 cycles, its products 1024, the
+// exponentials 1024; the rest is the latency of handing S and P over.
+#include <algorithm>
 #include <cfloat>
 #include <climits>
 
@@ -468,9 +475,16 @@ cudaError_t rows_of(const AttnParams& p, unsigned grid, cudaStream_t s) {
 
 }  // namespace
 
+// A CTA's step costs the same however many of its rows are there, about as much as attn.cu
+// needs for 48 to 58 rows on one SM. So: that many rows for each SM and for each CTA, by the
+// average length of a sequence's part (us here and there: 16 x 8 tokens behind 4096, 64/8
+// heads: 65 and 115; 32 x 16 and 32 x 8 behind 2048, 32/8 heads: 73 and 127, 71 and 67; 256
+// and 128 tokens behind 8192: 160 and 173, 161 and 102).
 bool attn_rows_serves(const AttnParams& p, int D) {
+    constexpr int kWorth = 48;
     const int64_t rows = (int64_t)p.T * (p.q.heads / p.cache.heads);  // of a cache head
-    return D == kD && rows >= (int64_t)kRows * p.B && rows / kRows * p.cache.heads >= device_sms() &&
+    const int64_t ctas = (rows / p.B + kBlock - 1) / kBlock * p.B * p.cache.heads;
+    return D == kD && rows * p.cache.heads >= kWorth * std::max<int64_t>(ctas, device_sms()) &&
            (rows / kBlock + p.B) * p.cache.heads < INT_MAX;
 }
 

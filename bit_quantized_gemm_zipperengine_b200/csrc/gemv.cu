@@ -1,7 +1,10 @@
 // Products of a few tokens of 16-bit activations with the packed NVFP4 weight:
 //   Y[m,n] = rn(g_w * sum_k x[m,k] (wh[n,k] + [block selected] rh[n,k])),  wh = val * dec(sf).
 //
-// What bounds it: the weight's bytes (9/16 a weight, 2304 a residual block), read once.
+// What bounds it: the weight's bytes (9/16 a weight, 2304 a residual block), read once, and
+// with them the conversions and products, which fill half of the issue slots: 1 token through
+// 28672 x 8192 with a tenth of the blocks takes 37.7 us (3.9 TB/s), 16 through 5120 x 25600
+// 30.0 us (14.3 for the copies alone), 1 through 4096 x 4096 8.4 us (4.4).
 //
 // The work of 64 weight rows is a list of steps: 256 columns of the base each, then four
 // residual blocks each (a block row's blocks lie one behind the other). In both a lane of
@@ -13,11 +16,11 @@
 //
 // The weights are the 16-row operand of fp16 tensor-core products (val * dec(sf) is exact
 // in fp16), eight tokens the other one. A first kernel writes the activations as that operand: in
-// fp16, bf16 ones scaled by a power of two per token (the largest element to [2^14, 2^15); what falls
-// below is under 2^-39 of it), in the order in which lanes read them. Formed inside the products'
-// kernel instead, by every CTA again, they cost it a fifth to a half of its time (16 tokens through
-// 14336 x 4096: 28.3 us against 18.3; one through 28672 x 8192: 45.1 against 43.4). The two kernels overlap: the weight's copies do not wait for
-// the first one.
+// fp16, bf16 ones scaled by a power of two per token (the largest element to [2^14, 2^15); what
+// falls below is under 2^-39 of it), in the order in which lanes read them. Formed inside the
+// products' kernel instead, by every CTA again, they cost it up to half of its time (16
+// tokens through 14336 x 4096: 28.3 us against 17.8). The two kernels overlap: the weight's
+// copies do not wait for the first one.
 //
 // The steps of a row tile are dealt to the pairs of a cluster of S CTAs, S so that the CTAs
 // about fill the GPU; the warps' sums are added in their order through shared memory, then

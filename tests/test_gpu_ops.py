@@ -444,6 +444,50 @@ def test_attention_many_rows(case, dtype, dev, mosaic):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+def test_attention_many_rows_single_tokens(dev, mosaic):
+    """One query token a sequence (no cu_q), 64 query heads on one."""
+    lens = [(37 * i) % 290 for i in range(130)]
+    q, pages, ks, vs, table, kv_len, cu = attn_inputs(lens, [1] * 130, 64, 1, 128, 16, BF, 95, dev)
+    want = ref.attention(q, pages, ks, vs, table, lens, [1] * 130, 0.09, 100)
+    o, lse = run_attn(mosaic, q, pages, ks, vs, table, kv_len, cu, 1, 0.09, 100, BF, False)
+    within(o, want[0], attn_bounds(*want, BF, lens)[0])
+    assert (o[want[1] == -math.inf] == 0).all()
+
+
+def test_attention_many_rows_in_graphs(dev, mosaic):
+    """A captured prompt replayed with other lengths, between calls of the other kernel and a
+    product that holds tensor memory too."""
+    lens, nqs = [700, 640], [300, 301]
+    q, pages, ks, vs, table, kv_len, cu = attn_inputs(lens, nqs, 64, 16, 128, 64, BF, 97, dev)
+    cache = mosaic.KVCache(pages, ks, vs)
+    out, small = torch.empty_like(q).contiguous(), torch.empty(2, 64, 128, dtype=BF, device=dev)
+    ws = mosaic.kv_attention_workspace(q, cache, 301)
+    layer = mosaic.Layer(256, 512, 3, dev)
+    layer.prepare_path(to_dev(synth.weight(256, 512, 1, 2, 0.06, 40, 2, 8.0), dev), to_dev(synth.act(128, 512, 3, 4, 4, 5.0), dev))
+    X = torch.randn(64, 512, generator=torch.Generator().manual_seed(1)).to(BF).to(dev)
+
+    def call():
+        y = layer.forward(X)
+        mosaic.mq_kv_attention(q, cache, table, kv_len, out, 0.09, cu, 301, ws=ws)
+        mosaic.mq_kv_attention(q[:2], cache, table, kv_len, small, 0.09, ws=ws)
+        return y, layer.forward(X)
+
+    y = call()[0].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ys = call()
+    for now in (lens, [320, 301], [1, 640]):
+        kv_len.copy_(torch.tensor(now, dtype=torch.int32))
+        for _ in range(3):
+            graph.replay()
+        want = ref.attention(q, pages, ks, vs, table, now, nqs, 0.09, 0)
+        within(out, want[0], attn_bounds(*want, BF, lens)[0], str(now))
+        want = ref.attention(q[:2], pages, ks, vs, table, now, [1, 1], 0.09, 0)
+        within(small, want[0], attn_bounds(*want, BF, lens)[0], str(now))
+        assert torch.equal(ys[0], y) and torch.equal(ys[1], y)
+
+
 def test_attention_many_rows_bad_pages_and_nan(dev, mosaic):
     """A page that is not there leaves its tokens out, as the same cache without them would; a
     NaN in a query stays in its row; rows of no sequence stay as they were."""
