@@ -150,8 +150,9 @@ size_t mq_kv_attention_workspace_bytes(int q_heads, int kv_heads, int D, int max
  * enter the second product in fp16. Rows of q that belong to no sequence leave out and lse
  * as they were. A page outside the cache, a length past the table (or 2^30) or a row past T is
  * left out and reported. q, out: [T][q heads][D] (distinct); lse: fp32 [T][q heads] or NULL.
- * max_q: the largest number of query tokens of a sequence that the caller expects (it
- * picks the kernel and sizes ws; more are served too). q heads a multiple of cache heads.
+ * max_q: the largest number of query tokens of a sequence that the caller expects (it sizes
+ * ws and, with the call's other sizes, picks the kernel; more are served too). q heads a
+ * multiple of cache heads.
  * Repeated calls give the same bits. T >= 0, B >= 0.
  */
 mq_status mq_kv_attention(const mq_heads* q, const mq_heads* out, float* lse, int T, mq_dtype type,
