@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) k_heads(const HeadsP
                     uint32_t sf;
                     const uint32_t codes = quantize_pair(a, g, __fmul_rn(6.0f, g), sf);
                     if (on && rec) {
-                        uint8_t* r = rec + (int64_t)h * ((p.cache.page_size >> 4) * (18 * D));
+                        uint8_t* r = rec + (int64_t)h * (p.cache.page_size >> 4) * (18 * D);
                         const int q = li >> 1;
                         const int at = c.kind == 1 ? tok * (D / 2) + 4 * li : rec_vcodes<D>(tok, q) + 4 * (li & 1);
                         *reinterpret_cast<uint32_t*>(r + at) = codes;
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(32 * kReadWarps) k_kv_read(const HeadsParams p
     int tok;
     split_slot(p, slot, page, tok);
     const int64_t per_head = (int64_t)(p.cache.page_size >> 4) * (18 * D);
-    const uint8_t* rec = p.cache.pages + page * H * per_head + (tok >> 4) * (18 * D);
+    const uint8_t* rec = p.cache.pages + page * H * per_head + (int64_t)(tok >> 4) * (18 * D);
     tok &= 15;
     const int kat = tok * (D / 2) + 4 * li, vat = rec_vcodes<D>(tok, q) + 4 * (li & 1);
     const int ksat = rec_kscale<D>(tok, q), vsat = rec_vscale<D>(tok, q);

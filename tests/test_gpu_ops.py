@@ -637,6 +637,39 @@ def test_cache_past_32_bits(dev, mosaic):
     within(o, want[0], attn_bounds(*want, BF, [n])[0])
 
 
+def test_page_past_31_bits(dev, mosaic):
+    """A page so large that its heads, and records inside a head, lie further apart than 2^31
+    bytes: written, read back and attended to at both ends of both heads."""
+    H, D, P, n = 2, 128, 2 ** 24, 90
+    cache = mosaic.KVCache(torch.empty((1, H, P // 16, 18 * D), dtype=torch.uint8, device=dev))
+    gen = torch.Generator().manual_seed(6)
+    for first in (0, P - n):
+        slots = first + torch.arange(n, device=dev)
+        k, v = (torch.randn(n, H, D, generator=gen).to(BF).to(dev) for _ in range(2))
+        k2, v2 = (torch.randn(n, H, D, generator=gen).to(BF).to(dev) for _ in range(2))
+        mosaic.mq_kv_append(k, v, slots, cache)
+        ko, vo = torch.empty_like(k), torch.empty_like(v)
+        mosaic.mq_kv_read(cache, slots, ko, vo)
+        for x, got in ((k, ko), (v, vo)):
+            assert torch.equal(got.cpu(), torch.from_numpy(oracle_rows(x, None)[2]).to(BF)), first
+        mosaic.mq_qkv_append(k2, k2, v2, torch.empty_like(k2), slots, cache)  # without norms and rotation
+        mosaic.mq_kv_read(cache, slots, ko, vo)
+        for x, got in ((k2, ko), (v2, vo)):
+            assert torch.equal(got.cpu(), torch.from_numpy(oracle_rows(x, None)[2]).to(BF)), first
+    # the page's last tokens alone, through a window
+    q = torch.randn(1, 16, D, generator=gen).to(BF).to(dev)
+    K, V = (torch.from_numpy(oracle_rows(x, None)[2]).to(dev).double() for x in (k2, v2))
+    z = torch.einsum("hgd,nhd->hgn", q[0].double().view(H, -1, D), K) * 0.09
+    p = torch.softmax(z, -1)
+    want, mass = torch.einsum("hgn,nhd->hgd", p, V), torch.einsum("hgn,nhd->hgd", p, V.abs())
+    smax = (0.09 * torch.einsum("hgd,nhd->hgn", q[0].double().abs().view(H, -1, D), K.abs())).amax(-1)
+    lse, vmax = torch.logsumexp(z, -1), torch.full_like(smax, float(V.abs().max()))
+    table, lens = torch.zeros(1, 1, dtype=torch.int32, device=dev), torch.tensor([P], dtype=torch.int32, device=dev)
+    o, _ = run_attn(mosaic, q, cache.pages, None, None, table, lens, None, 1, 0.09, n, BF, False)
+    flat = [x.reshape(1, 16, *x.shape[2:]) for x in (want, lse, mass, smax, vmax)]
+    within(o, flat[0], attn_bounds(*flat, BF, [n])[0])
+
+
 def test_attention_leaves_other_rows(dev, mosaic):
     lens, nqs = [50, 20], [2, 3]
     q, pages, ks, vs, table, kv_len, cu = attn_inputs(lens, nqs, 4, 2, 64, 16, HF, 31, dev)
