@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
     };
     auto record = [&](const Run& r, int j) -> const uint8_t* {
         const int pg = (int)p.by_page.div(j);
-        const int page = __ldg(p.table + r.b * p.table_stride + pg);
+        const int page = ld_prior(p.table + r.b * p.table_stride + pg);
         if (page < 0 || page >= p.cache.num_pages) return nullptr;
         return p.cache.pages + (((int64_t)page * H + r.h) * (p.cache.page_size >> 4) + ((j - pg * p.cache.page_size) >> 4)) * REC;
     };
@@ -283,8 +283,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
         // ---------------------------------------------------------------- one run, or this CTA's part of it
         const Seq& s = c.s;
         const int h = c.h, r0 = c.r0, end = c.end;
-        const float gk = p.cache.k_scale ? __ldg(p.cache.k_scale + h) : 1.0f;
-        const float gv = p.cache.v_scale ? __ldg(p.cache.v_scale + h) : 1.0f;
+        const float gk = p.cache.k_scale ? ld_prior(p.cache.k_scale + h) : 1.0f;
+        const float gv = p.cache.v_scale ? ld_prior(p.cache.v_scale + h) : 1.0f;
         const int first = first_of(c);
 
         // this lane's query elements (row 8 nt + g, d = t D/4 ...) as the second operand, and
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
                                                                   (int64_t)(h * G.d + row - qi * G.d) * p.q.sh + t * (D / 4));
 #pragma unroll
                 for (int i = 0; i < KS / 2; ++i) {
-                    const uint4 v = __ldg(src + i);
+                    const uint4 v = ld_prior(src + i);
                     qf[nt][2 * i][0] = v.x;
                     qf[nt][2 * i][1] = v.y;
                     qf[nt][2 * i + 1][0] = v.z;

@@ -22,10 +22,10 @@ struct Seq {
 };
 __device__ __forceinline__ Seq seq_of(const AttnParams& p, int b, bool report) {
     Seq s;
-    s.row0 = p.cu_q ? __ldg(p.cu_q + b) : b;
-    const int hi = p.cu_q ? __ldg(p.cu_q + b + 1) : b + 1;
+    s.row0 = p.cu_q ? ld_prior(p.cu_q + b) : b;
+    const int hi = p.cu_q ? ld_prior(p.cu_q + b + 1) : b + 1;
     s.nq = hi - s.row0;
-    s.len = __ldg(p.kv_len + b);
+    s.len = ld_prior(p.kv_len + b);
     if (s.row0 < 0 || hi < s.row0 || hi > p.T) {
         if (report) report_index(p.err);
         s.row0 = s.nq = 0;

@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_rows(const AttnParams p) {
             // a step's page number (looked at a step later, when it has arrived), and its record
             auto page_of = [&](int step) {
                 const int j = begin + step * kTile + 16 * r;
-                return step < steps && j < end ? __ldg(table + p.by_page.div(j)) : 0;
+                return step < steps && j < end ? ld_prior(table + p.by_page.div(j)) : 0;
             };
             auto record = [&](int step, int page) -> const uint8_t* {
                 const int j = begin + step * kTile + 16 * r;
@@ -211,12 +211,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_rows(const AttnParams p) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int i = n8 + 8 * u;
-                    kc[u] = __ldg(reinterpret_cast<const uint4*>(rec + i * (kD / 2) + 16 * t));
-                    ks[u] = __ldg(reinterpret_cast<const uint16_t*>(rec + rec_kscale<kD>(i, 2 * t)));
+                    kc[u] = ld_prior(reinterpret_cast<const uint4*>(rec + i * (kD / 2) + 16 * t));
+                    ks[u] = ld_prior(reinterpret_cast<const uint16_t*>(rec + rec_kscale<kD>(i, 2 * t)));
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
-                        vc[2 * u + w] = __ldg(reinterpret_cast<const uint2*>(rec + rec_vcodes<kD>(i, t + 4 * w)));
-                        vs[2 * u + w] = __ldg(rec + rec_vscale<kD>(i, t + 4 * w));
+                        vc[2 * u + w] = ld_prior(reinterpret_cast<const uint2*>(rec + rec_vcodes<kD>(i, t + 4 * w)));
+                        vs[2 * u + w] = ld_prior(rec + rec_vscale<kD>(i, t + 4 * w));
                     }
                 }
             };
@@ -318,12 +318,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_rows(const AttnParams p) {
             const bool on = row < rows;
             const int qi = on ? (int)G.div(row) : 0, hq = h * G.d + row - qi * G.d;
             const int64_t tok = s.row0 + qi;
-            const float gk = p.cache.k_scale ? __ldg(p.cache.k_scale + h) : 1.0f;
-            const float gv = p.cache.v_scale ? __ldg(p.cache.v_scale + h) : 1.0f;
+            const float gk = p.cache.k_scale ? ld_prior(p.cache.k_scale + h) : 1.0f;
+            const float gv = p.cache.v_scale ? ld_prior(p.cache.v_scale + h) : 1.0f;
             float inv = 1.0f;
             {
                 const uint4* src = reinterpret_cast<const uint4*>(p.q.p + tok * p.q.st + hq * p.q.sh);
-                auto piece = [&](int c) { return on ? __ldg(src + c) : make_uint4(0, 0, 0, 0); };
+                auto piece = [&](int c) { return on ? ld_prior(src + c) : make_uint4(0, 0, 0, 0); };
                 const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;  // the sign of the scale goes into the query: qs > 0
                 float up = 1.0f;
                 if constexpr (!F16) {

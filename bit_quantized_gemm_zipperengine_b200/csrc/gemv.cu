@@ -55,8 +55,8 @@ size_t operand_bytes(int nt, int K) { return (size_t)(K / 64) * nt * 1024 + 8 * 
 
 // A CTA a token (those past M: zeros).
 template <bool F16>
-__global__ void __launch_bounds__(kXThreads) k_gemv_x(const uint16_t* __restrict__ X, int64_t ldx, int M, int NT, int K,
-                                                      uint8_t* __restrict__ out, float* __restrict__ back) {
+__global__ void __launch_bounds__(kXThreads) k_gemv_x(const uint16_t* X, int64_t ldx, int M, int NT, int K, uint8_t* out,
+                                                      float* back) {
     __shared__ uint32_t tops[kXThreads / 32];
     const int m = blockIdx.x, pieces = K / 8;
     griddep_wait();
@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kXThreads) k_gemv_x(const uint16_t* __restrict
 #pragma unroll
     for (int i = 0; i < kXKeep; ++i) {
         const int c = threadIdx.x + i * kXThreads;
-        keep[i] = m < M && c < pieces ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        keep[i] = m < M && c < pieces ? ld_prior(src + c) : make_uint4(0, 0, 0, 0);
     }
     uint32_t ex = 15u;
     if constexpr (!F16) {
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kXThreads) k_gemv_x(const uint16_t* __restrict
 #pragma unroll
         for (int i = 0; i < kXKeep; ++i) a = __vmaxu2(a, top_of(keep[i]));
         if (m < M)
-            for (int c = threadIdx.x + kXKeep * kXThreads; c < pieces; c += kXThreads) a = __vmaxu2(a, top_of(__ldg(src + c)));
+            for (int c = threadIdx.x + kXKeep * kXThreads; c < pieces; c += kXThreads) a = __vmaxu2(a, top_of(ld_prior(src + c)));
         const uint32_t top = __reduce_max_sync(0xffffffffu, max(a & 0xFFFFu, a >> 16));
         if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
         __syncthreads();
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kXThreads) k_gemv_x(const uint16_t* __restrict
         if (c < pieces) put(c, keep[i]);
     }
     for (int c = threadIdx.x + kXKeep * kXThreads; c < pieces; c += kXThreads)
-        put(c, m < M ? __ldg(src + c) : make_uint4(0, 0, 0, 0));
+        put(c, m < M ? ld_prior(src + c) : make_uint4(0, 0, 0, 0));
     if (threadIdx.x == 0) back[m] = F16 ? 1.0f : __uint_as_float((ex - 14u) << 23);
 }
 
@@ -153,8 +153,8 @@ __global__ void __launch_bounds__(64 * pairs<NT>(), kCtasPerSm) k_gemv(const __g
         }
     };
     // The operand's kernel lets this one start after its own wait: all that came before it, the
-    // weight's writers among them, has ended. The first base steps fly before the residual's
-    // extent is known.
+    // weight's writers among them, has ended, so the weight is final (__ldg may read it). The
+    // first base steps fly before the residual's extent is known.
     int ahead = 0;
     while (ahead < kStages && step0 + ahead * stride < nbase) issue(ahead++);
     if (p.blk_codes) {
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(64 * pairs<NT>(), kCtasPerSm) k_gemv(const __g
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int w = 0; w < 4; ++w)
-                b[nt][w] = kt >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + nt * 1024 + w * 128)) : make_uint4(0, 0, 0, 0);
+                b[nt][w] = kt >= 0 ? ld_prior(reinterpret_cast<const uint4*>(src + nt * 1024 + w * 128)) : make_uint4(0, 0, 0, 0);
     };
     load_x(kt);
 
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(64 * pairs<NT>(), kCtasPerSm) k_gemv(const __g
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) v += sums[(w * 8 * NT + m) * kPitch + n];
         if (S == 1)
-            p.Y[m * p.ldy + tile * kRows + n] = (uint16_t)narrow2<F16>(v * __ldg(back + m) * gw, 0.0f);
+            p.Y[m * p.ldy + tile * kRows + n] = (uint16_t)narrow2<F16>(v * ld_prior(back + m) * gw, 0.0f);
         else
             mine[m * kPitch + n] = v;
     }
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(64 * pairs<NT>(), kCtasPerSm) k_gemv(const __g
             const int m = i / kRows, n = i % kRows;
             float v = 0.0f;
             for (int r = 0; r < S; ++r) v += ld_dsmem_f32(mine + m * kPitch + n, r);
-            p.Y[m * p.ldy + tile * kRows + n] = (uint16_t)narrow2<F16>(v * __ldg(back + m) * gw, 0.0f);
+            p.Y[m * p.ldy + tile * kRows + n] = (uint16_t)narrow2<F16>(v * ld_prior(back + m) * gw, 0.0f);
         }
         cluster_sync();  // no CTA leaves while another reads its sums
     }

@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) k_heads(const HeadsP
     uint8_t* rec = nullptr;  // head 0's record of this token's slot
     int tok = 0;             // its token in the record
     if (p.cache.pages) {
-        const int64_t slot = __ldg(p.slots + t);
+        const int64_t slot = ld_prior(p.slots + t);
         if (slot >= (int64_t)p.cache.num_pages * p.cache.page_size) {
             if (threadIdx.x == 0) report_index(p.err);
         } else if (slot >= 0) {
@@ -127,8 +127,8 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) k_heads(const HeadsP
     float2 cs[8];
     const int r2 = p.rot / 16, from = (lane & ~(LPR - 1)) + (li < r2 ? li + r2 : li < 2 * r2 ? li - r2 : li);
     if constexpr (TURN != 0) {
-        const double pos = (double)__ldg(p.pos + t);
-        for (int i = threadIdx.x; i < half; i += 32 * kWarps) angles[i] = cos_sin(pos, __ldg(p.freq + i));
+        const double pos = (double)ld_prior(p.pos + t);
+        for (int i = threadIdx.x; i < half; i += 32 * kWarps) angles[i] = cos_sin(pos, ld_prior(p.freq + i));
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < (TURN == 2 ? 4 : 8); ++j) {
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) k_heads(const HeadsP
 #pragma unroll
                     for (int x = 1; x < LPR; x <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, x);
                     const float r = rsqrtf(ss * (1.0f / D) + p.eps);
-                    const uint4 g = __ldg(reinterpret_cast<const uint4*>(wt + e0));
+                    const uint4 g = ld_prior(reinterpret_cast<const uint4*>(wt + e0));
                     const uint32_t x[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) k_heads(const HeadsP
                         a[2 * j] = f.x;
                         a[2 * j + 1] = f.y;
                     }
-                    const float g = sc && on ? __ldg(sc + h) : 1.0f;
+                    const float g = sc && on ? ld_prior(sc + h) : 1.0f;
                     uint32_t sf;
                     const uint32_t codes = quantize_pair(a, g, __fmul_rn(6.0f, g), sf);
                     if (on && rec) {
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(32 * kReadWarps) k_kv_read(const HeadsParams p
     const int H = p.cache.heads;
     griddep_wait();
     griddep_launch();
-    const int64_t slot = __ldg(p.slots + t);
+    const int64_t slot = ld_prior(p.slots + t);
     if (slot < 0) return;
     if (slot >= (int64_t)p.cache.num_pages * p.cache.page_size) {
         if (threadIdx.x == 0) report_index(p.err);
@@ -270,8 +270,8 @@ __global__ void __launch_bounds__(32 * kReadWarps) k_kv_read(const HeadsParams p
             vc[u] = *reinterpret_cast<const uint32_t*>(r + vat);
             ks[u] = r[ksat];
             vs[u] = r[vsat];
-            gk[u] = p.cache.k_scale ? __ldg(p.cache.k_scale + h) : 1.0f;
-            gv[u] = p.cache.v_scale ? __ldg(p.cache.v_scale + h) : 1.0f;
+            gk[u] = p.cache.k_scale ? ld_prior(p.cache.k_scale + h) : 1.0f;
+            gv[u] = p.cache.v_scale ? ld_prior(p.cache.v_scale + h) : 1.0f;
         }
 #pragma unroll
         for (int u = 0; u < kReadUnroll; ++u) {

@@ -159,6 +159,43 @@ def test_gemv_graphs_streams_and_workspaces(dev, mosaic):
         assert torch.equal(o, again)
 
 
+def test_gemv_reads_what_the_kernel_before_it_writes(dev, mosaic):
+    """Activations, and operands of attention, written over and over by the launch just before:
+    every call sees its own, not the call's before it."""
+    N, K, M, n = 256, 1024, 8, 24
+    base, packed = ref.random_weight(N, K, 9, 5, dev)
+    w = mosaic.Weight(base, packed)
+    gen = torch.Generator().manual_seed(7)
+    src = torch.randn(n, M, K // 128, 128, generator=gen).to(BF).to(dev)
+    x, ys = torch.empty(M, K // 128, 128, dtype=BF, device=dev), torch.empty(n, M, N, dtype=BF, device=dev)
+    pages, ks, vs = ref.random_cache(4, 16, K // 128, 128, 3, dev)
+    cache = mosaic.KVCache(pages, ks, vs)
+    slots = torch.arange(M, device=dev)
+    table, lens = torch.zeros(1, 1, dtype=torch.int32, device=dev), torch.full((1,), M, dtype=torch.int32, device=dev)
+    cu = torch.tensor([0, M], dtype=torch.int32, device=dev)
+    os_, ws = torch.empty(n, M, K // 128, 128, dtype=BF, device=dev), mosaic.kv_attention_workspace(x, cache, M)
+
+    def chain(i):
+        mosaic.mq_qk_norm_rope(src[i], None, x, None)  # without norm and rotation: a copy
+        mosaic.mq_gemv(x.view(M, K), w, ys[i])
+        mosaic.mq_kv_append(x, x, slots, cache)
+        mosaic.mq_kv_attention(x, cache, table, lens, os_[i], 0.09, cu, M, ws=ws)
+
+    for i in range(n):
+        chain(i)
+        torch.cuda.synchronize()
+    want = ys.clone(), os_.clone()
+    ys.zero_(), os_.zero_()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in range(n):
+            chain(i)
+    for _ in range(10):
+        graph.replay()
+    assert torch.equal(ys, want[0]) and torch.equal(os_, want[1])
+
+
 def test_gemv_on_a_prepared_layer(dev, mosaic):
     """The buffers that the layer's own preparation wrote, next to mq_gemm on the same weight."""
     L = synth.layer("tiny")

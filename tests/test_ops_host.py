@@ -1,11 +1,14 @@
 """Host-side checks of the operators of include/mosaic_ops.h: refusals before any launch,
 sizes, and the cache layout's text (each byte of a record used once)."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
 
 import ops_ref as ref
+from bit_quantized_gemm_zipperengine_b200 import build
 
 
 @pytest.fixture(scope="module")
@@ -160,6 +163,18 @@ def test_attention_refusals(L, buf):
     if n:
         assert call(ws=None) == 3 and call(n=n - 1) == 3 and call(ws=ws + 8) == 3
     assert call(T=0) == 0 and call(B=0) == 0
+
+
+def test_read_only_loads_are_of_final_data_alone():
+    """The operators' kernels start before their predecessor ends. __ldg promises that what it reads
+    does not change while the kernel lives: only the packed weight, whose writers ended before."""
+    csrc = os.path.join(build.PKG, "csrc")
+    for name in ("attn.cu", "attn.cuh", "attn_rows.cu", "gemv.cu", "heads.cu", "half_mma.cuh", "ops.cuh"):
+        with open(os.path.join(csrc, name)) as f:
+            code = re.sub(r"//[^\n]*", "", f.read())
+        read = set(re.findall(r"__ldg\(\s*([\w.]+)", code))
+        assert read <= ({"p.tile_ptr", "p.blk_kt", "p.g_w"} if name == "gemv.cu" else set()), (name, read)
+        assert "__restrict__" not in code, name  # a const __restrict__ pointer makes the same promise
 
 
 def test_binding_refuses_cpu_tensors_and_wrong_types():
