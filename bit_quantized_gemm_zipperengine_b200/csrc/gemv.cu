@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(64 * pairs<NT>(), kCtasPerSm) k_gemv(const __g
             for (int c = 0; c < 4; ++c)
                 sums[(warp * 8 * NT + 8 * nt + 2 * t + (c & 1)) * kPitch + 16 * rt + g + 8 * (c >> 1)] = acc[rt][nt][c];
     __syncthreads();
+    // the tensor scale before the token's: a sum times a far token's scale alone may pass fp32's range
     const float gw = __ldg(p.g_w);
     const float* back = reinterpret_cast<const float*>(p.xop + (int64_t)KC * (NT * 1024));  // the tokens' scales
     float* mine = sums + kWarps * 8 * NT * kPitch;  // [token][kPitch], this CTA's
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(64 * pairs<NT>(), kCtasPerSm) k_gemv(const __g
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) v += sums[(w * 8 * NT + m) * kPitch + n];
         if (S == 1)
-            p.Y[m * p.ldy + tile * kRows + n] = (uint16_t)narrow2<F16>(v * ld_prior(back + m) * gw, 0.0f);
+            p.Y[m * p.ldy + tile * kRows + n] = (uint16_t)narrow2<F16>(v * gw * ld_prior(back + m), 0.0f);
         else
             mine[m * kPitch + n] = v;
     }
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(64 * pairs<NT>(), kCtasPerSm) k_gemv(const __g
             const int m = i / kRows, n = i % kRows;
             float v = 0.0f;
             for (int r = 0; r < S; ++r) v += ld_dsmem_f32(mine + m * kPitch + n, r);
-            p.Y[m * p.ldy + tile * kRows + n] = (uint16_t)narrow2<F16>(v * ld_prior(back + m) * gw, 0.0f);
+            p.Y[m * p.ldy + tile * kRows + n] = (uint16_t)narrow2<F16>(v * gw * ld_prior(back + m), 0.0f);
         }
         cluster_sync();  // no CTA leaves while another reads its sums
     }

@@ -123,6 +123,22 @@ def test_gemv_far_magnitudes(big, dev, mosaic):
     within(y, want, gemv_bound(x, W, want, 2.0 ** -20, BF, K))
 
 
+@pytest.mark.parametrize("big,g", [(1e36, 2.0 ** -20), (2.0 ** 125, 2.0 ** -36), (1e-37, 2.0 ** -10), (1e-38, 2.0 ** 30)])
+def test_gemv_magnitudes_at_the_ends_of_bf16(big, g, dev, mosaic):
+    """Activations near bf16's largest and smallest values, whose products' sums pass fp32's range
+    before the tensor scale and lie inside it after."""
+    N, K, M = 128, 512, 3
+    base, packed = ref.random_weight(N, K, 5, 8, dev)
+    base["gscale"].fill_(g)
+    x = (torch.randn(M, K, generator=torch.Generator().manual_seed(2)).double() * torch.tensor([[big], [1.0], [big / 64]])).to(BF).to(dev)
+    W = ref.dense_weight(base, packed)
+    want = x.double() @ W.t() * g
+    assert torch.isfinite(x).all() and want.abs().max() < torch.finfo(BF).max
+    y = torch.full((M, N), math.nan, dtype=BF, device=dev)
+    mosaic.mq_gemv(x, mosaic.Weight(base, packed), y)
+    within(y, want, gemv_bound(x, W, want, g, BF, K))
+
+
 def test_gemv_graphs_streams_and_workspaces(dev, mosaic):
     """A captured call replayed with other activations, calls on two streams at once, and a
     workspace of the caller's that an earlier call left full."""
