@@ -72,7 +72,7 @@ mq_status mq_gemv(const void* X, mq_dtype type, int64_t ldx, const mq_nvfp4_mat*
         if (r->N != N || r->K != K || !r->blk_codes || !r->blk_sf || !r->blk_kt || !r->tile_ptr) return MQ_ERR_INVALID_ARG;
         if (!aligned(r->blk_codes, 16) || !aligned(r->blk_sf, 16)) return MQ_ERR_INVALID_ARG;
     }
-    if (M > 16) return MQ_ERR_UNSUPPORTED_SHAPE;
+    if (M > 16 || N / 64 > 65535) return MQ_ERR_UNSUPPORTED_SHAPE;  // a grid's second axis counts the row tiles
     if (!ws || ws_bytes < mq_gemv_workspace_bytes(M, K) || !aligned(ws, 16)) return MQ_ERR_WORKSPACE;
     const bool has_r = r && r->nblk > 0 && !(flags & MQ_GEMM_BASE_ONLY);
     GemvParams p;

@@ -73,8 +73,8 @@ size_t mq_kv_cache_bytes(int num_pages, int page_size, int heads, int D);
  *   Y[m,n] = rn( g_w * sum_k x[m,k] * ( wh[n,k] + [block (n/64, k/64) selected] rh[n,k] ) ),
  * wh and rh the scaled E2M1 values (val * dec(sf)), the sum in fp32. X: [M][K], row m at
  * m * ldx elements (16-byte aligned, ldx % 8 == 0); Y: [M][N], row m at m * ldy.
- * 1 <= M <= 16 tokens (MQ_ERR_UNSUPPORTED_SHAPE above: mq_gemm serves those), any N and K
- * that are multiples of 64. wq: codes, sf_swz (both 16-byte aligned), gscale [1]. r as in
+ * 1 <= M <= 16 tokens (MQ_ERR_UNSUPPORTED_SHAPE above: mq_gemm serves those), N and K any
+ * multiples of 64 (N up to 64 * 65535, MQ_ERR_UNSUPPORTED_SHAPE above). wq: codes, sf_swz (both 16-byte aligned), gscale [1]. r as in
  * mq_gemm, with blk_kt; blocks that tile_ptr puts past the store and columns that blk_kt puts
  * past K are left out and reported. flags: 0 or MQ_GEMM_BASE_ONLY / MQ_GEMM_RESIDUAL_ONLY;
  * MQ_GEMM_WEIGHTS_READY is taken and changes nothing (the weight is read while the activations

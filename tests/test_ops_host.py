@@ -84,6 +84,16 @@ def test_gemv_refusals(L, buf):
     assert call(w=mosaic.NVFP4Mat(N, K, w.codes + 8, None, w.sf_swz, w.gscale)) == 1
 
 
+def test_gemv_refuses_more_rows_than_a_grid_counts(L, buf):
+    """Before any launch: a launch that fails would leave its error for the next CUDA call."""
+    from bit_quantized_gemm_zipperengine_b200 import mosaic
+    p, K = buf(1 << 12), 64
+    for N, want in ((64 * 65536, 2), (2 ** 31 - 64, 2)):
+        w = mosaic.NVFP4Mat(N, K, p, None, p, p)
+        n = L.mq_gemv_workspace_bytes(1, K)
+        assert L.mq_gemv(p, 0, K, ctypes.byref(w), None, p, N, 1, N, K, 0, p, n, None) == want
+
+
 def test_rope_and_append_refusals(L, buf):
     from bit_quantized_gemm_zipperengine_b200 import mosaic
     T, D = 4, 64
