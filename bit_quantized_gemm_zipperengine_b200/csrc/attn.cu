@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
             }
             // never zero: a masked score is -inf before the scale (with this least scale every
             // other score rounds to 0)
-            const float z = fmaxf(inv * gk * fabsf(p.scale), FLT_MIN);
+            const float z = fmaxf(inv * (gk * fabsf(p.scale)), FLT_MIN);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 qs[nt][c] = __shfl_sync(0xffffffffu, z, 4 * (2 * t + c));

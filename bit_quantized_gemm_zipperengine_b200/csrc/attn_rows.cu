@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_rows(const AttnParams p) {
             fence_proxy_async_smem();
             mbar_arrive(q_full + g);
             // never zero: a masked score is -inf before the scale
-            const float qs = fmaxf(inv * gk * fabsf(p.scale), FLT_MIN);
+            const float qs = fmaxf(inv * (gk * fabsf(p.scale)), FLT_MIN);
             const int lim = on ? s.len - s.nq + qi + 1 : INT_MAX;
             const int lim_first = s.len - s.nq + (int)G.div(r0) + 1;
             const uint32_t mine = tmem + g * kCols + ((uint32_t)((warp & 3) * 32) << 16);  // this warp's lanes

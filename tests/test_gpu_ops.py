@@ -608,6 +608,22 @@ def test_attention_query_beyond_fp16(dev, mosaic):
         within(lse, want[1], bl, "lse")
 
 
+@pytest.mark.parametrize("rows", [False, True])
+def test_attention_smallest_queries(rows, dev, mosaic):
+    """bf16 queries near the smallest normal value with a scale that brings the scores back, in
+    both kernels: the scale of a row is not rounded to a subnormal on the way."""
+    lens, nqs = ([700, 301], [300, 301]) if rows else ([300], [4])
+    q, pages, ks, vs, table, kv_len, cu = attn_inputs(lens, nqs, 64 if rows else 8, 16 if rows else 2, 128, 32, BF, 13, dev)
+    q, ks = (q.float() * 2.0 ** -122).to(BF), ks * 2.0 ** -9
+    scale = 2.0 ** 124
+    want = ref.attention(q, pages, ks, vs, table, lens, nqs, scale, 0)
+    assert want[3].max() < 200
+    o, lse = run_attn(mosaic, q, pages, ks, vs, table, kv_len, cu, max(nqs), scale, 0, BF)
+    bo, bl = attn_bounds(*want, BF, lens)
+    within(o, want[0], bo, "out")
+    within(lse, want[1], bl, "lse")
+
+
 def test_attention_nan_queries(dev, mosaic):
     """A query row that holds a NaN gives NaN for itself, its lse too, and for no other row."""
     lens, nqs = [1500, 40, 0], [1, 3, 1]
