@@ -585,10 +585,16 @@ class AttentionLayer:
         # graphs that may run together, and be zeroed by the first one only.
         if torch.cuda.is_current_stream_capturing():
             return kv_attention_workspace(q, self.cache, max_q)
-        key = (max_q, torch.cuda.current_stream(q.device))
-        if key not in self._ws:
-            self._ws[key] = kv_attention_workspace(q, self.cache, max_q)
-        return self._ws[key]
+        # One for each stream, large enough for every max_q met on it (the size does not fall as
+        # max_q grows): calls of all shapes may take turns on a workspace.
+        key = torch.cuda.current_stream(q.device)
+        served, ws = self._ws.get(key, (0, None))
+        if max_q > served:
+            more = kv_attention_workspace(q, self.cache, max_q)
+            if ws is None or more is None or more.numel() > ws.numel():
+                ws = more
+            self._ws[key] = max_q, ws
+        return ws
 
     def step(self, X, pos, slots, block_table, kv_len, cu_q=None, max_q: int = 1, stream=None, ws=None):
         """One pass of the T new tokens X [T][hidden] (bf16; fp16 up to 16 tokens): their keys

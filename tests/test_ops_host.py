@@ -187,6 +187,36 @@ def test_read_only_loads_are_of_final_data_alone():
         assert "__restrict__" not in code, name  # a const __restrict__ pointer makes the same promise
 
 
+def test_attention_layer_keeps_one_workspace_a_stream(L, monkeypatch):
+    """Prompts of many lengths leave one buffer a stream, as large as the largest call's; the size
+    does not fall as max_q grows, so what serves a call serves those of fewer query tokens."""
+    from types import SimpleNamespace
+    from bit_quantized_gemm_zipperengine_b200 import mosaic
+    sizes = [L.mq_kv_attention_workspace_bytes(32, 8, 128, q) for q in range(1, 100)]
+    assert sizes == sorted(sizes) and 0 < sizes[0] < sizes[-1]
+    now = ["a"]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: now[0])
+    made = []
+
+    def workspace(q, cache, max_q=1):
+        made.append(torch.zeros(L.mq_kv_attention_workspace_bytes(q.shape[1], cache.heads, cache.D, max_q), dtype=torch.uint8))
+        return made[-1]
+
+    monkeypatch.setattr(mosaic, "kv_attention_workspace", workspace)
+    cache, q = SimpleNamespace(heads=8, D=128), torch.zeros(1, 32, 128)
+    layer = mosaic.AttentionLayer(SimpleNamespace(N=48 * 128), SimpleNamespace(K=32 * 128), 32, cache, None)
+    for max_q in list(range(1, 60)) + [7, 4096, 1, 33]:
+        ws = layer._workspace(q, max_q)
+        assert ws.numel() >= L.mq_kv_attention_workspace_bytes(32, 8, 128, max_q)
+    assert ws is layer._workspace(q, 5000) is layer._workspace(q, 1)
+    assert sum(w.numel() for _, w in layer._ws.values()) == sizes[-1]
+    now[0] = "b"
+    assert layer._workspace(q, 9) is not ws and len(layer._ws) == 2
+    now[0] = "a"
+    assert layer._workspace(q, 2) is ws
+
+
 def test_binding_refuses_cpu_tensors_and_wrong_types():
     from bit_quantized_gemm_zipperengine_b200 import mosaic
     pages = torch.zeros(2, 2, 1, 1152, dtype=torch.uint8)
