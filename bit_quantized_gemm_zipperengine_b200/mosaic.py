@@ -473,6 +473,7 @@ class Layer:
         self.sel = torch.empty(max(budget, 1), dtype=torch.int32, device=device)
         self.packed = alloc_packed(N, K, budget, device)
         self._act = {}
+        self._ws = {}  # of forward_fresh: stream -> ((M, flags) of the last call, workspace)
 
     def prepare(self, W: torch.Tensor, Xcal: torch.Tensor, stream=None):
         """A1..A5 through the separate calls (quantize, H, Delta + top-K, pack)."""
@@ -537,6 +538,42 @@ class Layer:
         mq_gemm(xq, self.base, self.packed, Y, M, self.N, self.K, flags, ws, stream)
         return Y
 
+    def _gemm_workspace(self, M: int, flags: int, stream: int):
+        """mq_gemm's workspace for M tokens on the current stream: one a stream, as large as any
+        call needed. Where its counters lie goes by M, and a call leaves its own at zero: they are
+        cleared when M changes. A captured call has its own, cleared at every replay."""
+        n = lib().mq_gemm_workspace_bytes(M, self.N, self.K, flags)
+        if n == 0:
+            return None
+        captured = torch.cuda.is_current_stream_capturing()
+        last, ws = (None, None) if captured else self._ws.get(stream, (None, None))
+        if last != (M, flags):
+            if ws is None or ws.numel() < n:
+                ws = _u8(n, device=self.device)
+            # the last bytes of the n: a counter for 16 x 64 outputs, or for more of them
+            ws[max(0, n - 4 * -(-M // 16) * (self.N // 64)):n].zero_()
+            if not captured:
+                self._ws[stream] = (M, flags), ws
+        return ws
+
+    def forward_fresh(self, X: torch.Tensor, flags: int = 0) -> torch.Tensor:
+        """forward on the current stream with buffers of this call alone (the workspace: of the
+        stream's calls): the result is a new tensor, nothing is kept for this number of tokens,
+        and calls on several streams or in captured graphs share no buffer."""
+        L, (M, K), s = lib(), X.shape, _stream()
+        codes = M * K // 2
+        sf = codes + -(-M // 128) * 8 * K  # rows in tiles of 128, a byte for 16 columns
+        buf = torch.empty(sf + 4 * M, dtype=torch.uint8, device=X.device)
+        p = buf.data_ptr()
+        xq = NVFP4Mat(M, K, p, None, p + codes, p + sf)
+        ws = self._gemm_workspace(M, flags, s.value)
+        w = self.weight
+        Y = torch.empty((M, self.N), dtype=torch.bfloat16, device=X.device)
+        _check(L.mq_quantize_act(_ptr(X), M, K, ctypes.byref(xq), s), "mq_quantize_act")
+        _check(L.mq_gemm(ctypes.byref(xq), ctypes.byref(w._mat), None if w._res is None else ctypes.byref(w._res), Y.data_ptr(),
+                         M, self.N, K, flags, *((None, 0) if ws is None else (ws.data_ptr(), ws.numel())), s), "mq_gemm")
+        return Y
+
     @property
     def weight(self) -> Weight:
         """The packed weight as mq_gemv takes it (built once; it reads the same buffers)."""
@@ -578,7 +615,7 @@ class AttentionLayer:
             return layer.forward_16bit(X)
         if X.dtype != torch.bfloat16:
             raise MosaicError("more than 16 tokens are taken in bf16")
-        return layer.forward(X)
+        return layer.forward_fresh(X)
 
     def _workspace(self, q, max_q):
         # A captured call gets its own, zeroed at every replay: one kept here would be shared by
@@ -599,10 +636,10 @@ class AttentionLayer:
     def step(self, X, pos, slots, block_table, kv_len, cu_q=None, max_q: int = 1, stream=None, ws=None):
         """One pass of the T new tokens X [T][hidden] (bf16; fp16 up to 16 tokens): their keys
         and values are appended at slots, then they attend to their sequences. kv_len counts
-        them. Tokens of one sequence are adjacent (cu_q). Every stream and every captured call
-        has its own workspace (ws: kv_attention_workspace(q, cache, max_q) of the caller's), so
-        calls of up to 16 tokens may overlap on different streams; calls of more tokens use the
-        layers' own buffers (see Layer.forward) and must not."""
+        them. Tokens of one sequence are adjacent (cu_q). Returns a new tensor. Every stream and
+        every captured call has its own buffers (ws: kv_attention_workspace(q, cache, max_q) of the
+        caller's), so calls may overlap on different streams, as far as the cache's pages and the
+        caller's ws allow it."""
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.step(X, pos, slots, block_table, kv_len, cu_q, max_q, None, ws)

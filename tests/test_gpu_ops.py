@@ -836,6 +836,102 @@ def test_attention_layer(norm, dev, mosaic):
         step(nqs)
 
 
+def prompt_layer(mosaic, dev, hidden=256, Hq=4, H=2, D=64, P=16, n=64):
+    """A layer with a cache of n tokens for each of two sequences, and a call for its prompts."""
+    qkv, proj = mosaic.Layer((Hq + 2 * H) * D, hidden, 6, dev), mosaic.Layer(hidden, Hq * D, 4, dev)
+    for i, l in enumerate((qkv, proj)):
+        l.prepare_path(to_dev(synth.weight(l.N, l.K, 40 + i, 44, 0.06, 40, 2, 8.0), dev), to_dev(synth.act(128, l.K, 46 + i, 48, 4, 5.0), dev))
+    freq = (1e4 ** (-2.0 * torch.arange(D // 2, dtype=torch.float64) / D)).to(dev)
+    layer = mosaic.AttentionLayer(qkv, proj, Hq, mosaic.KVCache.alloc(2 * n // P, P, H, D, dev), freq)
+    table = torch.arange(2 * n // P, dtype=torch.int32, device=dev).view(2, -1)
+
+    def prompt(X, b=0, **more):
+        T = X.shape[0]
+        pos = torch.arange(T, device=dev)
+        slots = table[b, pos // P].long() * P + pos % P
+        cu = torch.tensor([0, T], dtype=torch.int32, device=dev)
+        lens = torch.tensor([T], dtype=torch.int32, device=dev)
+        t = table[b:b + 1].contiguous()
+        return lambda X=X: layer.step(X, pos, slots, t, lens, cu, T, **more)
+
+    return layer, prompt
+
+
+def tokens(T, seed, dev, hidden=256):
+    return torch.randn(T, hidden, generator=torch.Generator().manual_seed(seed)).to(BF).to(dev)
+
+
+def test_attention_layer_prompts_have_results_of_their_own(dev, mosaic):
+    """A step's result stays as it is when the layer takes other prompts of as many tokens, on
+    other streams too, and prompts of many lengths leave nothing behind in the layers."""
+    layer, prompt = prompt_layer(mosaic, dev)
+    Xs = [tokens(40, i, dev) for i in range(4)]
+    want = [prompt(X)().clone() for X in Xs]
+    got = [prompt(X)() for X in Xs]
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.equal(layer._project(layer.qkv, Xs[0]), layer.qkv.forward(Xs[0]))  # the path's own result
+    kept = len(layer.qkv._act), len(layer.out._act)
+    for T in range(17, 64):
+        prompt(tokens(T, T, dev))()
+    assert (len(layer.qkv._act), len(layer.out._act)) == kept
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    calls = [prompt(X, b, stream=s) for b, (X, s) in enumerate(zip(Xs, streams))]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        outs = [c() for c in calls]
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
+def test_layer_forward_fresh_and_its_workspace(dev, mosaic):
+    """Numbers of tokens whose products need a workspace, in any order, eager and captured: the
+    results of forward; one workspace a stream."""
+    N, K = 2048, 4096
+    layer = mosaic.Layer(N, K, 100, dev)
+    gen = torch.Generator().manual_seed(3)
+    layer.prepare_path((0.02 * torch.randn(N, K, generator=gen)).to(BF).to(dev), tokens(128, 5, dev, K))
+    Ms = (48, 128, 17, 100, 48, 64, 128, 200, 64)
+    assert sum(mosaic.lib().mq_gemm_workspace_bytes(M, N, K, 0) > 0 for M in Ms) > 5
+    Xs = [tokens(M, M, dev, K) for M in Ms]
+    want = [layer.forward(X).clone() for X in Xs]
+    for _ in range(3):
+        got = [layer.forward_fresh(X) for X in Xs]
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert len(layer._ws) == 1
+    flags = mosaic.MQ_GEMM_BASE_ONLY
+    base = layer.forward(Xs[0], flags).clone()
+    assert torch.equal(layer.forward_fresh(Xs[0], flags), base) and torch.equal(layer.forward_fresh(Xs[0]), want[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = [layer.forward_fresh(X) for X in Xs]
+    assert len(layer._ws) == 1
+    for _ in range(3):
+        assert torch.equal(layer.forward_fresh(Xs[3]), want[3])
+        graph.replay()
+        assert torch.equal(layer.forward_fresh(Xs[3]), want[3])
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_attention_layer_captured_prompt_before_an_eager_one(dev, mosaic):
+    """The first call of a number of tokens is captured; eager ones of as many do not meet the
+    graph's memory, before a replay or after it."""
+    layer, prompt = prompt_layer(mosaic, dev)
+    X, Y = tokens(48, 1, dev), tokens(48, 2, dev)
+    call, other = prompt(X, 0), prompt(Y, 1)
+    prompt(tokens(20, 3, dev))()  # the library's first use, with other sizes
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    eager = other()
+    again = call().clone()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        graph.replay()
+        assert torch.equal(other(), eager) and torch.equal(out, again)
+
+
 def test_attention_layer_in_graphs(dev, mosaic):
     """Two captured steps of one layer and eager ones, in any order and at once: each has a
     workspace of its own, and a graph replayed first is not the one that was captured first."""
