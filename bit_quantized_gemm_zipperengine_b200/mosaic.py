@@ -557,9 +557,12 @@ class Layer:
         return ws
 
     def forward_fresh(self, X: torch.Tensor, flags: int = 0) -> torch.Tensor:
-        """forward on the current stream with buffers of this call alone (the workspace: of the
+        """forward, of strided X too, on the current stream with buffers of this call alone (the workspace: of the
         stream's calls): the result is a new tensor, nothing is kept for this number of tokens,
         and calls on several streams or in captured graphs share no buffer."""
+        if X.dtype != torch.bfloat16 or X.dim() != 2 or X.shape[1] != self.K:
+            raise MosaicError(f"X [M][{self.K}] in bf16 is wanted, got {tuple(X.shape)} of {X.dtype}")
+        X = X.contiguous()
         L, (M, K), s = lib(), X.shape, _stream()
         codes = M * K // 2
         sf = codes + -(-M // 128) * 8 * K  # rows in tiles of 128, a byte for 16 columns

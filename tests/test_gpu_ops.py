@@ -883,6 +883,19 @@ def test_attention_layer_prompts_have_results_of_their_own(dev, mosaic):
     assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
 
 
+def test_attention_layer_strided_tokens(dev, mosaic):
+    """Tokens that are rows of a wider tensor give what their copies give, few and many of them."""
+    layer, prompt = prompt_layer(mosaic, dev)
+    for T in (5, 16, 17, 40):
+        wide = torch.randn(T, 256 + 72, generator=torch.Generator().manual_seed(T)).to(BF).to(dev)
+        X = wide[:, 8:8 + 256]
+        want = prompt(X.contiguous())()
+        assert torch.equal(prompt(X)(), want), T
+    for bad in (wide, wide[:, :128].contiguous(), X.float()):
+        with pytest.raises(mosaic.MosaicError):
+            prompt(bad)()
+
+
 def test_layer_forward_fresh_and_its_workspace(dev, mosaic):
     """Numbers of tokens whose products need a workspace, in any order, eager and captured: the
     results of forward; one workspace a stream."""
