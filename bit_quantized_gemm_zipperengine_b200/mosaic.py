@@ -646,6 +646,11 @@ class AttentionLayer:
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.step(X, pos, slots, block_table, kv_len, cu_q, max_q, None, ws)
+        if not X.is_cuda:
+            raise MosaicError("libmosaic takes CUDA tensors only")
+        if X.get_device() != torch.cuda.current_device():
+            with torch.cuda.device(X.get_device()):
+                return self.step(X, pos, slots, block_table, kv_len, cu_q, max_q, None, ws)
         T, D, H, Hq = X.shape[0], self.cache.D, self.cache.heads, self.q_heads
         if T == 0:
             return X.new_empty((0, self.out.N))

@@ -217,6 +217,41 @@ def test_attention_layer_keeps_one_workspace_a_stream(L, monkeypatch):
     assert layer._workspace(q, 2) is ws
 
 
+def test_attention_layer_runs_on_the_device_of_its_tokens(monkeypatch):
+    """With another device current, the whole step, prompts' projections among it, is launched with
+    the tokens' device current, and the caller's device is current again after it."""
+    from types import SimpleNamespace
+    from bit_quantized_gemm_zipperengine_b200 import mosaic
+    at, seen = [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, at[0] = at[0], self.index
+
+        def __exit__(self, *a):
+            at[0] = self.before
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: at[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+
+    class Layer(mosaic.AttentionLayer):
+        def _project(self, layer, X):
+            seen.append(at[0])
+            raise KeyError  # nothing is launched here
+
+    layer = Layer(SimpleNamespace(N=48 * 128), SimpleNamespace(K=32 * 128), 32, SimpleNamespace(heads=8, D=128), None)
+    for dev in (1, 0):
+        X = SimpleNamespace(shape=(20, 256), is_cuda=True, get_device=lambda: dev)
+        with pytest.raises(KeyError):
+            layer.step(X, None, None, None, None)
+    assert seen == [1, 0] and at == [0]
+    with pytest.raises(mosaic.MosaicError):
+        layer.step(torch.zeros(20, 256, dtype=torch.bfloat16), None, None, None, None)
+
+
 def test_binding_refuses_cpu_tensors_and_wrong_types():
     from bit_quantized_gemm_zipperengine_b200 import mosaic
     pages = torch.zeros(2, 2, 1, 1152, dtype=torch.uint8)
