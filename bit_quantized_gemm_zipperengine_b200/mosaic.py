@@ -498,34 +498,41 @@ class Layer:
         mq_topk_blocks(self.delta, self.budget, self.rank, self.sel, stream)
         mq_pack_residual_weight(W, self.base, self.sel, self.budget, self.packed, stream)
 
+    def _kept(self, key, make):
+        """The tensors that make() gives, kept for the next call with this key. What a captured call
+        makes lies in its graph's memory, and is zeroed by a replay alone: the call keeps it to itself."""
+        if key in self._act:
+            return self._act[key]
+        made = make()
+        if not torch.cuda.is_current_stream_capturing():
+            self._act[key] = made
+        return made
+
     def act_buffers(self, M: int, flags: int = 0, slot: int = 0):
         """Quantized X, Y and the GEMM workspace for M tokens (cached per M, flags and slot:
         calls in flight together on different streams take different slots)."""
-        key = (M, flags, slot)
-        if key not in self._act:
-            self._act[key] = (alloc_act(M, self.K, self.device),
-                              torch.empty((M, self.N), dtype=torch.bfloat16, device=self.device),
-                              gemm_workspace(M, self.N, self.K, flags, self.device))
-        return self._act[key]
+        return self._kept((M, flags, slot), lambda: (
+            alloc_act(M, self.K, self.device), torch.empty((M, self.N), dtype=torch.bfloat16, device=self.device),
+            gemm_workspace(M, self.N, self.K, flags, self.device)))
 
     def buffers(self, M: int, T: int, flags: int = 0, staging: bool = False, slot: int = 0) -> LayerBuffers:
         """The ctypes struct mq_run_layer takes (staging buffers for host inputs). Every slot
         has its own activation and staging buffers; the layer's weights are shared."""
         xq, Y, ws = self.act_buffers(M, flags, slot)
         b = LayerBuffers()
+        b.act = xq, Y, ws  # alive as long as the pointers
         b.base, b.resid_full, b.xq = mat(self.base), mat(self.resid), mat(xq)
         b.H, b.delta, b.rank, b.sel = _ptr(self.H), _ptr(self.delta), _ptr(self.rank), _ptr(self.sel)
         b.packed = packed_struct(self.packed)
         b.ws_quant, b.ws_quant_bytes = _ptr(self.qws), self.qws.numel()
         b.ws_gemm, b.ws_gemm_bytes = (_ptr(ws), ws.numel()) if ws is not None else (None, 0)
         if staging:
-            key = ("staging", M, T, slot)
-            if key not in self._act:
-                bf = torch.bfloat16
-                self._act[key] = (torch.empty((self.N, self.K), dtype=bf, device=self.device),
-                                  torch.empty((M, self.K), dtype=bf, device=self.device),
-                                  torch.empty((T, self.K), dtype=bf, device=self.device))
-            w, x, xc = self._act[key]
+            bf = torch.bfloat16
+            w, x, xc = self._kept(("staging", M, T, slot), lambda: (
+                torch.empty((self.N, self.K), dtype=bf, device=self.device),
+                torch.empty((M, self.K), dtype=bf, device=self.device),
+                torch.empty((T, self.K), dtype=bf, device=self.device)))
+            b.staging = w, x, xc  # alive as long as the pointers
             b.W_dev, b.X_dev, b.Xcal_dev, b.Y_dev = _ptr(w), _ptr(x), _ptr(xc), _ptr(Y)
         return b
 

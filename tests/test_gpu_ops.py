@@ -926,6 +926,30 @@ def test_layer_forward_fresh_and_its_workspace(dev, mosaic):
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
 
 
+def test_layer_captured_call_keeps_its_buffers_to_itself(dev, mosaic):
+    """A first call of some number of tokens inside a capture: eager calls of as many get buffers of
+    their own, with a workspace that is zero before any replay."""
+    N, K, M = 2048, 4096, 64
+    layer = mosaic.Layer(N, K, 100, dev)
+    gen = torch.Generator().manual_seed(4)
+    layer.prepare_path((0.02 * torch.randn(N, K, generator=gen)).to(BF).to(dev), tokens(128, 5, dev, K))
+    X, Z = tokens(M, 1, dev, K), tokens(M, 2, dev, K)
+    layer.forward(tokens(M + 1, 1, dev, K))  # the library's first use, with another number of tokens
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = layer.forward(X)
+        buf = layer.buffers(M, 128, slot=1)
+    assert not any(key[0] == M for key in layer._act) and buf.ws_gemm == buf.act[2].data_ptr()
+    eager = layer.forward(Z)
+    assert eager.data_ptr() != out.data_ptr() and layer.forward(Z) is eager
+    want, wantX = layer.forward_fresh(Z), layer.forward_fresh(X)
+    for _ in range(3):
+        graph.replay()
+        assert torch.equal(eager, want) and torch.equal(out, wantX)
+        assert torch.equal(layer.forward(Z), want) and torch.equal(out, wantX)
+
+
 def test_attention_layer_captured_prompt_before_an_eager_one(dev, mosaic):
     """The first call of a number of tokens is captured; eager ones of as many do not meet the
     graph's memory, before a replay or after it."""
