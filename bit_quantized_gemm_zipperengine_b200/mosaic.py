@@ -9,9 +9,12 @@ library or a non-CUDA tensor raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
+
+from . import build
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmosaic.so")
@@ -358,9 +361,12 @@ def _ops():
     global _marshal
     if _marshal is None:
         L = lib()
-        if not os.path.exists(os.path.join(_PKG, "_marshal.so")):
-            raise MosaicError("_marshal.so is not built; run __graft_entry__.build()")
-        from . import _marshal as m
+        path = build.marshal_path()
+        if not os.path.exists(path):
+            raise MosaicError(f"{path} is not built; run __graft_entry__.build()")
+        spec = importlib.util.spec_from_file_location(__package__ + "._marshal", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
         m.bind(MosaicError, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
             "mq_gemv", "mq_qk_norm_rope", "mq_kv_append", "mq_qkv_append", "mq_kv_read", "mq_kv_attention",
             "mq_status_string", "mq_gemv_workspace_bytes")))

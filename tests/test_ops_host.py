@@ -252,6 +252,33 @@ def test_attention_layer_runs_on_the_device_of_its_tokens(monkeypatch):
         layer.step(torch.zeros(20, 256, dtype=torch.bfloat16), None, None, None, None)
 
 
+def test_the_library_is_built_without_the_extension(tmp_path, monkeypatch):
+    """The C library comes first and needs nvcc alone; the timeline's needs no extension at all; an
+    extension for another PyTorch is not taken for the running one's."""
+    ran = []
+
+    def call(cmd):
+        ran.append(cmd[0])
+        if cmd[0] != "nvcc":
+            raise FileNotFoundError(cmd[0])
+        with open(cmd[cmd.index("-o") + 1], "w"):
+            pass
+
+    real = build.marshal_path()
+    monkeypatch.setattr(build, "PKG", str(tmp_path))
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "lib.so"))
+    monkeypatch.setattr(build, "LIB_TIMELINE", str(tmp_path / "timeline.so"))
+    monkeypatch.setattr(build.subprocess, "check_call", call)
+    monkeypatch.delenv("NVCC", raising=False)
+    monkeypatch.delenv("CXX", raising=False)
+    with pytest.raises(FileNotFoundError):
+        build.build()
+    assert ran == ["nvcc", "g++"] and (tmp_path / "lib.so").exists() and not build.stale(build.LIB)
+    assert build.build(timeline=True) == build.LIB_TIMELINE and ran == ["nvcc", "g++", "nvcc"]
+    monkeypatch.setattr(build.importlib.metadata, "version", lambda name: "0.1")
+    assert os.path.basename(build.marshal_path()) != os.path.basename(real)
+
+
 def test_binding_refuses_cpu_tensors_and_wrong_types():
     from bit_quantized_gemm_zipperengine_b200 import mosaic
     pages = torch.zeros(2, 2, 1, 1152, dtype=torch.uint8)
