@@ -3,7 +3,7 @@
 //
 // What bounds it: the cache's bytes, 9/8 D a token and head, read once for all the query
 // rows of a cache head (a "row" is a query token and one of the query heads that share it).
-// Calls with many rows a cache head go to attn_rows.cu.
+// Calls with many rows a cache head and D = 128 go to attn_rows.cu.
 //
 // Once a long cache streams, the conversions, multiplies and products that share the issue slots
 // are the longer half: 4 x 131072 tokens, 64/8 heads take 127 us (4.8 TB/s), the copies alone

@@ -52,7 +52,7 @@ __device__ __forceinline__ float lse_of(float top, float sum) {
     return sum == 0.0f ? -INFINITY : (top - kShift + log2f(sum)) * 0.69314718055994531f;
 }
 
-// attn_rows.cu: tiles of 128 query rows; whether it serves a call (by_group, by_page and the
+// attn_rows.cu: tiles of 256 query rows, D = 128; whether it serves a call (by_group, by_page and the
 // scale set as for the other kernel)
 bool attn_rows_serves(const AttnParams& p, int D);
 cudaError_t launch_attn_rows(const AttnParams& p, bool f16, cudaStream_t s);

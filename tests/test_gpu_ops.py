@@ -667,6 +667,42 @@ def test_attention_bad_indices_are_reported_and_left_out(dev, mosaic):
     assert (o[1] == 77).all()
 
 
+def without_pages(table, lens, P, bad):
+    """Table and lengths of single-token sequences whose pages `bad` (b, i) are cut out: what is left
+    when a page is not there (the order of a sequence's tokens does not matter to its last one)."""
+    t, n = table.clone(), list(lens)
+    for b in range(len(lens)):
+        gone = {i for c, i in bad if c == b}
+        keep = [i for i in range(-(-lens[b] // P)) if i not in gone]
+        t[b, :len(keep)] = table[b, torch.tensor(keep, device=table.device, dtype=torch.long)]
+        n[b] = lens[b] - sum(min(P, lens[b] - i * P) for i in gone)
+    return t, n
+
+
+@pytest.mark.parametrize("lens,Hq,H,D,P,bad", [
+    ([100, 40], 8, 2, 128, 16, [(0, 2)]),
+    ([100, 47], 8, 2, 64, 16, [(0, 0), (0, 1), (1, 2)]),         # a whole step, and a last page in part
+    ([3000], 8, 2, 128, 48, [(0, 0), (0, 30), (0, 31), (0, 62)]),
+    # about 20 steps of every warp: pages of the first 16, which are looked up together, and behind them
+    ([140000], 16, 8, 64, 64, [(0, i) for i in (0, 1, 17, 31, 32, 33, 34, 35, 36, 37, 38, 39, 40, 700, 1331, 1332, 2000, 2186, 2187)]),
+    ([140000], 16, 8, 64, 64, [(0, i) for i in range(5, 2188, 13)]),
+])
+def test_attention_missing_pages_are_left_out(lens, Hq, H, D, P, bad, dev, mosaic):
+    """Single tokens whose sequences miss pages: the result of the tokens that are there."""
+    q, pages, ks, vs, table, kv_len, cu = attn_inputs(lens, [1] * len(lens), Hq, H, D, P, BF, 23, dev)
+    t2, n2 = without_pages(table, lens, P, bad)
+    want = ref.attention(q, pages, ks, vs, t2, n2, [1] * len(lens), 0.1, 0)
+    bo, bl = attn_bounds(*want, BF, lens)
+    for name in (-1, pages.shape[0]):
+        t = table.clone()
+        for b, i in bad:
+            t[b, i] = name
+        o, lse = run_attn(mosaic, q, pages, ks, vs, t, kv_len, cu, 1, 0.1, 0, BF, False)
+        assert mosaic.mq_get_error() == 1
+        within(o, want[0], bo, "out")
+        within(lse, want[1], bl, "lse")
+
+
 def test_attention_shapes_share_a_workspace(dev, mosaic):
     """Calls of different shapes take turns on one workspace, large enough for each: the partial
     sums of one leave the other's counters alone."""
