@@ -3,7 +3,7 @@
 //
 // What bounds it: the cache's bytes, 9/8 D a token and head, read once for all the query
 // rows of a cache head (a "row" is a query token and one of the query heads that share it).
-// Calls with many rows a cache head and D = 128 go to attn_rows.cu.
+// Calls, and sequences, with many rows a cache head and D = 128 go to attn_rows.cu (attn.cuh).
 //
 // Once a long cache streams, the conversions, multiplies and products that share the issue slots
 // are the longer half: 4 x 131072 tokens, 64/8 heads take 127 us (4.8 TB/s), the copies alone
@@ -29,6 +29,7 @@
 // units, wherever the sequences end. Runs that are cut leave partial sums in the workspace;
 // whoever finishes a run last adds its parts in their order, so the result does not depend on
 // the timing.
+#include <algorithm>
 #include <cfloat>
 #include <climits>
 
@@ -77,12 +78,6 @@ struct Run {
     int64_t unit0;
 };
 
-__device__ __forceinline__ int64_t warp_sum(int64_t v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -106,19 +101,48 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
     const FastDiv& G = p.by_group;
     if (tid < kWarps * kStages) mbar_init(&full[0][0] + tid, 2);  // the two records' lanes
     mbar_fence_init();
-    griddep_wait();
-    griddep_launch();
+    // With split, attn_rows.cu's kernel is the one before. It waited before it let this one start, so
+    // what this one reads is there, and the two may run side by side; the first CTA waits for it at
+    // its end, and lets the next kernel start no sooner.
+    if (!p.split) {
+        griddep_wait();
+        griddep_launch();
+    }
+    auto leave = [&] {
+        if (p.split && blockIdx.x == 0) {
+            griddep_wait();
+            griddep_launch();
+        }
+    };
 
     // The CTA's work. CTA w takes the w-th equal share of all units, in order; or, with fewer
     // runs than CTAs, every run is cut into equal pieces of at most q units, one CTA each. Then no
     // CTA joins two runs, which costs it about as much as kJoin units (16 sequences of up to
     // 8192 tokens: 33.2 us by shares, 31.8 by pieces; 4 of 131072, where pieces waste 5 of 74
     // units: 126.6 and 132.7).
-    const Seq own = tid < p.B ? seq_of(p, tid, blockIdx.x == 0) : Seq{0, 0, 0};
+    Seq own = tid < p.B ? seq_of(p, tid, blockIdx.x == 0) : Seq{0, 0, 0};
+    int64_t all_work = 0;
+    if (p.split) {
+        all_work = rows_work(own, p);
+        for (int b = tid + kThreads; b < p.B; b += kThreads) all_work += rows_work(seq_of(p, b, false), p);
+        all_work = warp_sum(all_work);
+        if (lane == 0) red[warp] = all_work;
+        __syncthreads();
+        all_work = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) all_work += red[w];
+        __syncthreads();
+    }
+    // a sequence; without query tokens if the other kernel has it
+    auto left = [&](Seq s) {
+        if (p.split && takes_rows(s, p, all_work)) s.nq = 0;
+        return s;
+    };
+    own = left(own);
     const int64_t own_units = seq_units(own, G, p.window, R) * H;
     int64_t mine = own_units, rmine = (int64_t)((own.nq * G.d + R - 1) / R) * H;
     for (int b = tid + kThreads; b < p.B; b += kThreads) {
-        const Seq s = seq_of(p, b, blockIdx.x == 0);
+        const Seq s = left(seq_of(p, b, blockIdx.x == 0));
         mine += seq_units(s, G, p.window, R) * H;
         rmine += (int64_t)((s.nq * G.d + R - 1) / R) * H;
     }
@@ -136,7 +160,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
         total += red[w];
         runs += red2[w];
     }
-    if (total == 0) return;
+    if (total == 0) {
+        leave();
+        return;
+    }
     const int grid = (int)gridDim.x;
     const bool fits = total < (1 << 30);  // 32-bit divisions
     const int64_t share = fits ? (int)p.by_grid.div((uint32_t)total + grid - 1) : (total + grid - 1) / grid;
@@ -165,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
         int64_t base = 0;
         for (int b0 = 0; b0 < p.B; b0 += kThreads) {
             const int b = b0 + tid;
-            const int64_t n = b0 == 0 ? own_n : b < p.B ? seq_units(seq_of(p, b, false), G, p.window, R) * H : 0;
+            const int64_t n = b0 == 0 ? own_n : b < p.B ? seq_units(left(seq_of(p, b, false)), G, p.window, R) * H : 0;
             int64_t x = n;  // inclusive scan over the CTA
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -191,7 +218,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
         }
         __syncthreads();
     }
-    if (found[0] < 0) return;  // past the last piece or unit
+    if (found[0] < 0) {  // past the last piece or unit
+        leave();
+        return;
+    }
     Run c;
     c.b = (int)found[0];
     c.s = seq_of(p, c.b, false);
@@ -567,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
                 nx.r0 = 0;
                 if (++nx.h == H) {
                     nx.h = 0;
-                    do nx.s = seq_of(p, ++nx.b, false);
+                    do nx.s = left(seq_of(p, ++nx.b, false));
                     while (nx.s.nq == 0);
                 }
             }
@@ -741,6 +771,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
     if (!alive)
         for (uint32_t i = 1; i <= min(given, (uint32_t)kStages); ++i)
             mbar_wait_err(&full[warp][(given - i) % kStages], ((given - i) / kStages) & 1u, p.err);
+    leave();
 }
 
 // Rings, then the memory of a merge: the warps' rows, or a run's factors (at most one part a CTA).
@@ -781,13 +812,22 @@ size_t attn_workspace(int q_heads, int kv_heads, int D, int max_q, size_t* parti
     return *partials_at + (size_t)2 * grid_of(nt) * slot_floats(nt, D) * sizeof(float);
 }
 
-cudaError_t launch_attn(const AttnParams& p0, int D, int max_q, bool f16, cudaStream_t s) {
+cudaError_t launch_attn(const AttnParams& p0, int D, int max_q, bool f16, cudaStream_t s, int* kernels) {
     AttnParams p = p0;
     p.by_group = FastDiv(p.q.heads / p.cache.heads);
     p.by_page = FastDiv(p.cache.page_size);
     p.scale *= 1.4426950408889634f;  // scores in powers of two
-    if (attn_rows_serves(p, D)) return launch_attn_rows(p, f16, s);
-    const int nt = row_tiles(p.q.heads, p.cache.heads, max_q), grid = grid_of(nt);
+    const AttnKernels which = attn_kernels(p, D, max_q);
+    int nt = row_tiles(p.q.heads, p.cache.heads, max_q);
+    if (which != AttnKernels::one) {
+        p.split = which == AttnKernels::both;
+        p.even = (int64_t)kRowsWorth * device_sms();
+        const cudaError_t e = launch_attn_rows(p, f16, s);
+        if (e != cudaSuccess || !p.split) return e;
+        *kernels = 2;
+        nt = std::min(nt, row_tiles(p.q.heads, p.cache.heads, 1));  // mostly single tokens are left
+    }
+    const int grid = grid_of(nt);
     p.by_grid = FastDiv(grid);
     if (D == 64) {
         if (nt == 1) return f16 ? attn_of<64, 1, true>(p, grid, s) : attn_of<64, 1, false>(p, grid, s);

@@ -16,6 +16,13 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Sum over the warp of values from 0 to 2^58, 22 bits at a time.
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
+    constexpr unsigned all = 0xffffffffu, low = (1u << 22) - 1;
+    const int64_t a = __reduce_add_sync(all, (unsigned)v & low), b = __reduce_add_sync(all, (unsigned)(v >> 22) & low),
+                  c = __reduce_add_sync(all, (unsigned)(v >> 44));
+    return a + (b << 22) + (c << 44);
+}
 // Sequence b: its rows of q and its length, checked.
 struct Seq {
     int row0, nq, len;
@@ -52,9 +59,31 @@ __device__ __forceinline__ float lse_of(float top, float sum) {
     return sum == 0.0f ? -INFINITY : (top - kShift + log2f(sum)) * 0.69314718055994531f;
 }
 
-// attn_rows.cu: tiles of 256 query rows, D = 128; whether it serves a call (by_group, by_page and the
-// scale set as for the other kernel)
-bool attn_rows_serves(const AttnParams& p, int D);
+// Which sequences of a call are whose. A CTA of attn_rows.cu takes a tile of kRowsTile query rows
+// through its tokens alone, kRowsStep a step, at a cost that does not go by how many rows there
+// are: about what the other kernel needs for kRowsWorth rows on one SM. The other kernel cuts any
+// sequence over all SMs. So attn_rows.cu is given a sequence with kRowsLeast rows or more (its
+// tiles hold kRowsWorth each then) if its chain of steps is not longer than an SM's even share of
+// what all such sequences cost in the other kernel. Both kernels find the same answer, from integers.
+constexpr int kRowsTile = 256, kRowsStep = 64, kRowsWorth = 48, kRowsLeast = 128;
+
+__device__ __forceinline__ int64_t rows_steps(const Seq& s, const AttnParams& p) {
+    return (p.window > 0 ? min((int64_t)s.len, (int64_t)p.window + s.nq) : (int64_t)s.len) / kRowsStep + 1;
+}
+// A sequence's query rows times steps, if it has the rows.
+__device__ __forceinline__ int64_t rows_work(const Seq& s, const AttnParams& p) {
+    const int64_t rows = s.nq * p.by_group.d;
+    return rows >= kRowsLeast ? rows * p.cache.heads * rows_steps(s, p) : 0;
+}
+// work: the sum over the call's sequences.
+__device__ __forceinline__ bool takes_rows(const Seq& s, const AttnParams& p, int64_t work) {
+    return s.nq * p.by_group.d >= kRowsLeast && rows_steps(s, p) * p.even <= work;
+}
+
+// attn_rows.cu: tiles of 256 query rows, D = 128 (by_group, by_page and the scale set as for the
+// other kernel). Which kernels a call runs:
+enum class AttnKernels { one, rows, both };
+AttnKernels attn_kernels(const AttnParams& p, int D, int max_q);
 cudaError_t launch_attn_rows(const AttnParams& p, bool f16, cudaStream_t s);
 
 }  // namespace mq

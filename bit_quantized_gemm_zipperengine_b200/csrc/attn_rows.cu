@@ -36,7 +36,8 @@ constexpr int kD = 128;
 constexpr int kRows = 128;   // query rows of an operand, one softmax thread each
 constexpr int kGroups = 2;   // operands of a CTA
 constexpr int kBlock = kGroups * kRows;
-constexpr int kTile = 64;    // tokens of a step
+constexpr int kTile = kRowsStep;  // tokens of a step
+static_assert(kBlock == kRowsTile);
 // Warps: one a group that issues its products, four that convert, four a group for the query rows.
 constexpr int kConvert = kGroups, kSoftmax = kConvert + 4;
 constexpr int kThreads = 32 * (kSoftmax + 4 * kGroups);
@@ -140,10 +141,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_rows(const AttnParams p) {
 
     // The CTA's tile: sequences in order, then tiles from the last rows on (they see most), then heads.
     if (warp == 0) {
+        const Seq own = lane < p.B ? seq_of(p, lane, blockIdx.x == 0) : Seq{0, 0, 0};
+        int64_t all_work = 0;
+        if (p.split) {
+            all_work = rows_work(own, p);
+            for (int b = lane + 32; b < p.B; b += 32) all_work += rows_work(seq_of(p, b, false), p);
+            all_work = warp_sum(all_work);
+        }
         int64_t base = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             const int b = b0 + lane;
-            const Seq s = b < p.B ? seq_of(p, b, blockIdx.x == 0) : Seq{0, 0, 0};
+            Seq s = b0 == 0 ? own : b < p.B ? seq_of(p, b, blockIdx.x == 0) : Seq{0, 0, 0};
+            if (p.split && !takes_rows(s, p, all_work)) s.nq = 0;
             const int64_t n = (int64_t)((s.nq * G.d + kBlock - 1) / kBlock) * H;
             int64_t x = n;
 #pragma unroll
@@ -476,21 +485,30 @@ cudaError_t rows_of(const AttnParams& p, unsigned grid, cudaStream_t s) {
 }  // namespace
 
 // A CTA's step costs the same however many of its rows are there, about as much as attn.cu
-// needs for 48 to 58 rows on one SM. So: that many rows for each SM and for each CTA, by the
-// average length of a sequence's part (us here and there: 16 x 8 tokens behind 4096, 64/8
+// needs for 48 to 58 rows on one SM. So, where all sequences have as many query tokens: that many
+// rows for each SM and for each CTA (us here and there: 16 x 8 tokens behind 4096, 64/8
 // heads: 65 and 115; 32 x 16 and 32 x 8 behind 2048, 32/8 heads: 73 and 127, 71 and 67; 256
-// and 128 tokens behind 8192: 160 and 173, 161 and 102).
-bool attn_rows_serves(const AttnParams& p, int D) {
-    constexpr int kWorth = 48;
-    const int64_t rows = (int64_t)p.T * (p.q.heads / p.cache.heads);  // of a cache head
+// and 128 tokens behind 8192: 160 and 173, 161 and 102). Where they may differ, and one may have
+// kRowsLeast rows, the kernels share the call, sequence by sequence (us by the average of all
+// sequences and by each one's own rows: a prompt of 2048 beside 15 single tokens behind 131072,
+// 64/8 heads: 1930 and 547; beside one behind 2^20, 32/8 heads: 14500 and 297; 512 tokens beside 15
+// single ones, all behind 8192: 239 and 161). The second kernel costs a call of prompts alone 1.5
+// us (1000 and 1024 tokens: 42.0 and 43.5).
+AttnKernels attn_kernels(const AttnParams& p, int D, int max_q) {
+    const int64_t G = p.q.heads / p.cache.heads, rows = p.T * G;  // of a cache head
+    const int64_t most = std::min<int64_t>(p.T, std::max(max_q, (int)(((int64_t)p.T + p.B - 1) / p.B)));  // query tokens of one sequence
+    if (D != kD || rows * p.cache.heads < (int64_t)kRowsWorth * device_sms() || (rows / kRows + p.B) * p.cache.heads >= INT_MAX)
+        return AttnKernels::one;
+    if (p.cu_q && p.T != p.B * most) return most * G >= kRowsLeast ? AttnKernels::both : AttnKernels::one;
     const int64_t ctas = (rows / p.B + kBlock - 1) / kBlock * p.B * p.cache.heads;
-    return D == kD && rows * p.cache.heads >= kWorth * std::max<int64_t>(ctas, device_sms()) &&
-           (rows / kBlock + p.B) * p.cache.heads < INT_MAX;
+    return rows * p.cache.heads >= kRowsWorth * ctas ? AttnKernels::rows : AttnKernels::one;
 }
 
 cudaError_t launch_attn_rows(const AttnParams& p, bool f16, cudaStream_t s) {
     const int64_t rows = (int64_t)p.T * (p.q.heads / p.cache.heads);
-    const unsigned grid = (unsigned)((rows / kBlock + p.B) * p.cache.heads);  // at most: every sequence ends in a part of a tile
+    // at most: every sequence that is taken ends in a part of a tile
+    const int64_t taken = p.split ? std::min<int64_t>(p.B, rows / kRowsLeast) : p.B;
+    const unsigned grid = (unsigned)((rows / kBlock + taken) * p.cache.heads);
     return f16 ? rows_of<true>(p, grid, s) : rows_of<false>(p, grid, s);
 }
 

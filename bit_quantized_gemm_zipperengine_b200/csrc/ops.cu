@@ -224,7 +224,9 @@ mq_status mq_kv_attention(const mq_heads* q, const mq_heads* out, float* lse, in
     p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + partials_at);
     p.err = device_error_word();
     if (!p.err) return MQ_ERR_CUDA;
-    return count_launches(launch_attn(p, D, max_q, type == MQ_F16, as_stream(stream)), 1);
+    int kernels = 1;
+    const cudaError_t e = launch_attn(p, D, max_q, type == MQ_F16, as_stream(stream), &kernels);
+    return count_launches(e, kernels);
 }
 
 }  // extern "C"

@@ -129,6 +129,8 @@ struct AttnParams {
     int* counters;
     int* err;
     FastDiv by_group, by_page, by_grid;  // query heads of a cache head, tokens of a page, CTAs
+    int split;                           // both kernels run: attn.cuh says which sequences are whose
+    int64_t even;                        // with split: kRowsWorth query rows for each SM
 };
 
 // api.cu: a launch's status, counted in mq_launch_count; the current device's error word
@@ -145,6 +147,7 @@ size_t gemv_workspace(int M, int K);
 cudaError_t launch_gemv(const CUtensorMap& tw, const GemvParams& p, bool f16, cudaStream_t s);
 // bytes: counters, then partial sums at *partials_at
 size_t attn_workspace(int q_heads, int kv_heads, int D, int max_q, size_t* partials_at);
-cudaError_t launch_attn(const AttnParams& p, int D, int max_q, bool f16, cudaStream_t s);
+// *kernels: how many were launched
+cudaError_t launch_attn(const AttnParams& p, int D, int max_q, bool f16, cudaStream_t s, int* kernels);
 
 }  // namespace mq

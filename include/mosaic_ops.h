@@ -151,7 +151,9 @@ size_t mq_kv_attention_workspace_bytes(int q_heads, int kv_heads, int D, int max
  * as they were. A page outside the cache, a length past the table (or 2^30) or a row past T is
  * left out and reported. q, out: [T][q heads][D] (distinct); lse: fp32 [T][q heads] or NULL.
  * max_q: the largest number of query tokens of a sequence that the caller expects (it sizes
- * ws and, with the call's other sizes, picks the kernel; more are served too). q heads a
+ * ws and, with the call's other sizes, picks the kernel; more are served too). Prompts and
+ * single tokens may share a call: T other than B * max_q says so, and each sequence goes to the
+ * kernel that its own rows and length ask for. q heads a
  * multiple of cache heads.
  * Repeated calls give the same bits. T >= 0, B >= 0.
  */

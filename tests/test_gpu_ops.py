@@ -497,6 +497,96 @@ def test_attention_many_rows(case, dtype, dev, mosaic):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+MIXED = [
+    # prompts beside single tokens and drafts, by two kernels: (query tokens, cached), Hq, H, P, window
+    ([(1, 700), (300, 301), (1, 5), (0, 40), (200, 200), (1, 0), (7, 90)], 64, 16, 16, 0),
+    ([(300, 300) if i in (0, 33, 69) else (1, (37 * i) % 150) for i in range(70)], 32, 16, 32, 0),
+    ([(260, 100 + i) if i in (5, 140) else (i % 3, (11 * i) % 90) for i in range(150)], 64, 16, 16, 60),
+    ([(64, 20000), (300, 300), (1, 129)], 64, 16, 64, 0),       # many rows, and too long for one CTA each
+    ([(1, 3000), (130, 40), (2, 1), (150, 1000)], 64, 16, 48, 0),  # more query tokens than cached
+    ([(31, 64), (32, 64), (33, 64), (200, 64)], 128, 32, 64, 0),   # beside the least rows
+]
+
+
+@pytest.mark.parametrize("case", range(len(MIXED)))
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_attention_mixed(case, dtype, dev, mosaic):
+    seqs, Hq, H, P, window = MIXED[case]
+    nqs, lens = [s[0] for s in seqs], [s[1] for s in seqs]
+    q, pages, ks, vs, table, kv_len, cu = attn_inputs(lens, nqs, Hq, H, 128, P, dtype, 170 + case, dev)
+    scale = (-1) ** case * 128 ** -0.5
+    want = ref.attention(q, pages, ks, vs, table, lens, nqs, scale, window)
+    bo, bl = attn_bounds(*want, dtype, lens)
+    dead = want[1] == -math.inf
+    q = torch.cat((q, q[:5]))  # rows of no sequence
+    first = None
+    for max_q in (max(nqs), 1, 10 * max(nqs)):
+        at = mosaic.mq_launch_count()
+        o, lse = run_attn(mosaic, q, pages, ks, vs, table, kv_len, cu, max_q, scale, window, dtype)
+        if max_q == max(nqs):
+            assert mosaic.mq_launch_count() == at + 2
+            first = o.clone(), lse.clone()
+        assert (o[-5:] == 77).all() and (lse[-5:] == 77).all()
+        o, lse = o[:-5], lse[:-5]
+        within(o, want[0], bo, "out")
+        assert (lse[dead] == -math.inf).all() and (o[dead] == 0).all()
+        within(lse[~dead], want[1][~dead], bl[~dead], "lse")
+    o, lse = run_attn(mosaic, q, pages, ks, vs, table, kv_len, cu, max(nqs), scale, window, dtype)
+    assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+    # a page that is not there, and a length past the table, in both kinds: the others as they were
+    for b in range(min(2, len(lens))):
+        if lens[b] > P:
+            t = table.clone()
+            t[b, 1] = pages.shape[0]
+            o, _ = run_attn(mosaic, q, pages, ks, vs, t, kv_len, cu, max(nqs), scale, window, dtype)
+            assert mosaic.mq_get_error() == 1
+            rest = torch.ones(sum(nqs), dtype=torch.bool, device=dev)
+            rest[int(cu[b]):int(cu[b + 1])] = False
+            within(o[:-5][rest], want[0][rest], bo[rest])
+
+
+def test_attention_mixed_in_graphs(dev, mosaic):
+    """A captured chain of calls, each the next one's queries, replayed with other rows and lengths:
+    which kernel has which sequence changes, and the next call sees what both wrote."""
+    B, T, Hq, H, P, most = 4, 400, 64, 16, 32, 512
+    q, pages, ks, vs, table, kv_len, cu = attn_inputs([most] * B, [100] * B, Hq, H, 128, P, BF, 190, dev)
+    q = q.contiguous()
+    cache = mosaic.KVCache(pages, ks, vs)
+    ws = mosaic.kv_attention_workspace(q, cache, T)
+    outs = [torch.empty_like(q) for _ in range(3)]
+
+    def chain(sync=False):
+        x = q
+        for o in outs:
+            mosaic.mq_kv_attention(x, cache, table, kv_len, o, 0.09, cu, T, ws=ws)
+            x = o
+            if sync:
+                torch.cuda.synchronize()
+
+    chain()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    for rows, lens in (([0, 300, 301, 302, 400], [300, 512, 1, 100]), ([0, 1, 2, 3, 400], [512, 0, 77, 397]),
+                       ([0, 100, 200, 300, 400], [512, 100, 300, 101]), ([0, 0, 0, 0, 400], [1, 2, 3, 400]),
+                       ([0, 400, 400, 400, 400], [64, 1, 1, 1]), ([0, 20, 40, 41, 60], [512, 500, 400, 300])):
+        cu.copy_(torch.tensor(rows, dtype=torch.int32))
+        kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
+        for o in outs:
+            o.fill_(0.5)
+        chain(sync=True)
+        want = [o.clone() for o in outs]
+        nqs = [b - a for a, b in zip(rows, rows[1:])]
+        w = ref.attention(q[:rows[-1]], pages, ks, vs, table, lens, nqs, 0.09, 0)
+        within(want[0][:rows[-1]], w[0], attn_bounds(*w, BF, lens)[0], str(rows))
+        for o in outs:
+            o.fill_(0.5)
+        for _ in range(3):
+            graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), rows
+
+
 def test_attention_many_rows_single_tokens(dev, mosaic):
     """One query token a sequence (no cu_q), 64 query heads on one."""
     lens = [(37 * i) % 290 for i in range(130)]
