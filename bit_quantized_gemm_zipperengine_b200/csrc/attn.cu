@@ -817,15 +817,16 @@ cudaError_t launch_attn(const AttnParams& p0, int D, int max_q, bool f16, cudaSt
     p.by_group = FastDiv(p.q.heads / p.cache.heads);
     p.by_page = FastDiv(p.cache.page_size);
     p.scale *= 1.4426950408889634f;  // scores in powers of two
-    const AttnKernels which = attn_kernels(p, D, max_q);
+    const AttnPlan plan = attn_plan(p, D, max_q);
     int nt = row_tiles(p.q.heads, p.cache.heads, max_q);
-    if (which != AttnKernels::one) {
-        p.split = which == AttnKernels::both;
+    if (plan.rows) {
+        p.split = plan.other;
+        p.least = plan.least;
         p.even = (int64_t)kRowsWorth * device_sms();
         const cudaError_t e = launch_attn_rows(p, f16, s);
         if (e != cudaSuccess || !p.split) return e;
         *kernels = 2;
-        nt = std::min(nt, row_tiles(p.q.heads, p.cache.heads, 1));  // mostly single tokens are left
+        if (plan.least == kRowsLeast) nt = std::min(nt, row_tiles(p.q.heads, p.cache.heads, 1));  // mostly single tokens are left
     }
     const int grid = grid_of(nt);
     p.by_grid = FastDiv(grid);

@@ -62,10 +62,11 @@ __device__ __forceinline__ float lse_of(float top, float sum) {
 // Which sequences of a call are whose. A CTA of attn_rows.cu takes a tile of kRowsTile query rows
 // through its tokens alone, kRowsStep a step, at a cost that does not go by how many rows there
 // are: about what the other kernel needs for kRowsWorth rows on one SM. The other kernel cuts any
-// sequence over all SMs. So attn_rows.cu is given a sequence with kRowsLeast rows or more (its
-// tiles hold kRowsWorth each then) if its chain of steps is not longer than an SM's even share of
-// what all such sequences cost in the other kernel. Both kernels find the same answer, from integers.
-constexpr int kRowsTile = 256, kRowsStep = 64, kRowsWorth = 48, kRowsLeast = 128;
+// sequence over all SMs. So attn_rows.cu is given a sequence with `least` rows or more (its tiles
+// hold kRowsWorth each then) if its chain of steps is not longer than an SM's even share of what
+// all such sequences cost in the other kernel. Both kernels find the same answer, from integers.
+constexpr int kRowsTile = 256, kRowsStep = 64, kRowsWorth = 48;
+constexpr int kRowsLeast = 128;  // `least` where the numbers of query tokens differ; below it where they do not
 
 __device__ __forceinline__ int64_t rows_steps(const Seq& s, const AttnParams& p) {
     return (p.window > 0 ? min((int64_t)s.len, (int64_t)p.window + s.nq) : (int64_t)s.len) / kRowsStep + 1;
@@ -73,17 +74,20 @@ __device__ __forceinline__ int64_t rows_steps(const Seq& s, const AttnParams& p)
 // A sequence's query rows times steps, if it has the rows.
 __device__ __forceinline__ int64_t rows_work(const Seq& s, const AttnParams& p) {
     const int64_t rows = s.nq * p.by_group.d;
-    return rows >= kRowsLeast ? rows * p.cache.heads * rows_steps(s, p) : 0;
+    return rows >= p.least ? rows * p.cache.heads * rows_steps(s, p) : 0;
 }
 // work: the sum over the call's sequences.
 __device__ __forceinline__ bool takes_rows(const Seq& s, const AttnParams& p, int64_t work) {
-    return s.nq * p.by_group.d >= kRowsLeast && rows_steps(s, p) * p.even <= work;
+    return s.nq * p.by_group.d >= p.least && rows_steps(s, p) * p.even <= work;
 }
 
 // attn_rows.cu: tiles of 256 query rows, D = 128 (by_group, by_page and the scale set as for the
-// other kernel). Which kernels a call runs:
-enum class AttnKernels { one, rows, both };
-AttnKernels attn_kernels(const AttnParams& p, int D, int max_q);
+// other kernel). Which kernels a call runs, and the rows of a sequence that may be that one's:
+struct AttnPlan {
+    bool other, rows;
+    int least;
+};
+AttnPlan attn_plan(const AttnParams& p, int D, int max_q);
 cudaError_t launch_attn_rows(const AttnParams& p, bool f16, cudaStream_t s);
 
 }  // namespace mq

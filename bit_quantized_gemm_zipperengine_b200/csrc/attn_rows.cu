@@ -488,26 +488,30 @@ cudaError_t rows_of(const AttnParams& p, unsigned grid, cudaStream_t s) {
 // needs for 48 to 58 rows on one SM. So, where all sequences have as many query tokens: that many
 // rows for each SM and for each CTA (us here and there: 16 x 8 tokens behind 4096, 64/8
 // heads: 65 and 115; 32 x 16 and 32 x 8 behind 2048, 32/8 heads: 73 and 127, 71 and 67; 256
-// and 128 tokens behind 8192: 160 and 173, 161 and 102). Where they may differ, and one may have
-// kRowsLeast rows, the kernels share the call, sequence by sequence (us by the average of all
-// sequences and by each one's own rows: a prompt of 2048 beside 15 single tokens behind 131072,
-// 64/8 heads: 1930 and 547; beside one behind 2^20, 32/8 heads: 14500 and 297; 512 tokens beside 15
-// single ones, all behind 8192: 239 and 161). The second kernel costs a call of prompts alone 1.5
-// us (1000 and 1024 tokens: 42.0 and 43.5).
-AttnKernels attn_kernels(const AttnParams& p, int D, int max_q) {
-    const int64_t G = p.q.heads / p.cache.heads, rows = p.T * G;  // of a cache head
-    const int64_t most = std::min<int64_t>(p.T, std::max(max_q, (int)(((int64_t)p.T + p.B - 1) / p.B)));  // query tokens of one sequence
-    if (D != kD || rows * p.cache.heads < (int64_t)kRowsWorth * device_sms() || (rows / kRows + p.B) * p.cache.heads >= INT_MAX)
-        return AttnKernels::one;
-    if (p.cu_q && p.T != p.B * most) return most * G >= kRowsLeast ? AttnKernels::both : AttnKernels::one;
-    const int64_t ctas = (rows / p.B + kBlock - 1) / kBlock * p.B * p.cache.heads;
-    return rows * p.cache.heads >= kRowsWorth * ctas ? AttnKernels::rows : AttnKernels::one;
+// and 128 tokens behind 8192: 160 and 173, 161 and 102). A sequence that fills the SMs by itself is
+// never worse off here, however long it is. If none does, or the numbers of query tokens differ,
+// the kernels share the call, sequence by sequence (us by the average of all sequences and by each
+// one's own rows: a prompt of 2048 beside 15 single tokens behind 131072, 64/8 heads: 1930 and 546;
+// beside one behind 2^20, 32/8 heads: 14500 and 296; 512 tokens beside 15 single ones, all behind
+// 8192: 239 and 163; 16 x 8 tokens behind 4096, one of them behind 131072, 64/8 heads: 1820 and
+// 251). A call that is all one kernel's pays 1 to 2% for it (16 x 8 behind 4096: 66.8 and 67.0; 32 x
+// 16 behind 2048: 72.2 and 73.6; eight prompts of 37 to 4000 tokens: 295 and 301).
+AttnPlan attn_plan(const AttnParams& p, int D, int max_q) {
+    const int64_t G = p.q.heads / p.cache.heads, H = p.cache.heads, rows = p.T * G;  // rows: of a cache head
+    const int64_t fill = (int64_t)kRowsWorth * device_sms();
+    const int64_t most = std::min<int64_t>(p.T, std::max<int64_t>(max_q, ((int64_t)p.T + p.B - 1) / p.B));  // query tokens of a sequence
+    const AttnPlan other = {true, false, 0};
+    if (D != kD || rows * H < fill || (rows / kRowsWorth + p.B) * H >= INT_MAX) return other;
+    if (p.T != p.B * most) return most * G >= kRowsLeast ? AttnPlan{true, true, kRowsLeast} : other;
+    const int64_t own = rows / p.B;
+    if (own < kRowsWorth * ((own + kBlock - 1) / kBlock)) return other;
+    return AttnPlan{p.B > 1 && own * H < fill, true, (int)std::min<int64_t>(own, kRowsLeast - 1)};
 }
 
 cudaError_t launch_attn_rows(const AttnParams& p, bool f16, cudaStream_t s) {
     const int64_t rows = (int64_t)p.T * (p.q.heads / p.cache.heads);
     // at most: every sequence that is taken ends in a part of a tile
-    const int64_t taken = p.split ? std::min<int64_t>(p.B, rows / kRowsLeast) : p.B;
+    const int64_t taken = p.split ? std::min<int64_t>(p.B, rows / p.least) : p.B;
     const unsigned grid = (unsigned)((rows / kBlock + taken) * p.cache.heads);
     return f16 ? rows_of<true>(p, grid, s) : rows_of<false>(p, grid, s);
 }

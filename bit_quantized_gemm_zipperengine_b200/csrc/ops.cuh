@@ -130,7 +130,8 @@ struct AttnParams {
     int* err;
     FastDiv by_group, by_page, by_grid;  // query heads of a cache head, tokens of a page, CTAs
     int split;                           // both kernels run: attn.cuh says which sequences are whose
-    int64_t even;                        // with split: kRowsWorth query rows for each SM
+    int least;                           // with split: the query rows of a sequence that it is about,
+    int64_t even;                        // and kRowsWorth rows for each SM
 };
 
 // api.cu: a launch's status, counted in mq_launch_count; the current device's error word

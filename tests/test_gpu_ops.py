@@ -545,6 +545,24 @@ def test_attention_mixed(case, dtype, dev, mosaic):
             within(o[:-5][rest], want[0][rest], bo[rest])
 
 
+@pytest.mark.parametrize("nq,B,Hq,H,long,window", [(8, 16, 64, 8, 9000, 0), (1, 130, 64, 1, 12000, 0), (13, 20, 32, 8, 700, 300)])
+def test_attention_as_many_tokens_each_and_ragged_lengths(nq, B, Hq, H, long, window, dev, mosaic):
+    """As many query tokens each, rows enough for the kernel of many rows, one context far longer."""
+    lens = [long if i == B // 2 else (37 * i) % 210 for i in range(B)]
+    q, pages, ks, vs, table, kv_len, cu = attn_inputs(lens, [nq] * B, Hq, H, 128, 16, BF, 200 + nq, dev)
+    want = ref.attention(q, pages, ks, vs, table, lens, [nq] * B, 0.09, window)
+    bo, bl = attn_bounds(*want, BF, lens)
+    dead = want[1] == -math.inf
+    at = mosaic.mq_launch_count()
+    o, lse = run_attn(mosaic, q, pages, ks, vs, table, kv_len, cu, nq, 0.09, window, BF, nq > 1)
+    assert mosaic.mq_launch_count() == at + 2
+    within(o, want[0], bo, "out")
+    assert (lse[dead] == -math.inf).all() and (o[dead] == 0).all()
+    within(lse[~dead], want[1][~dead], bl[~dead], "lse")
+    again = run_attn(mosaic, q, pages, ks, vs, table, kv_len, cu, nq, 0.09, window, BF, nq > 1)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
 def test_attention_mixed_in_graphs(dev, mosaic):
     """A captured chain of calls, each the next one's queries, replayed with other rows and lengths:
     which kernel has which sequence changes, and the next call sees what both wrote."""
