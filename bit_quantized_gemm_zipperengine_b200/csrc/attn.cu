@@ -83,7 +83,8 @@ __device__ __forceinline__ float warp_max(float v) {
     for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
-template <int D, int NT, bool F16>
+// SPLIT: attn_rows.cu's kernel has some of the sequences (attn.cuh).
+template <int D, int NT, bool F16, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const AttnParams p) {
     constexpr int R = 8 * NT;           // rows of a tile
     constexpr int REC = 18 * D;         // bytes of a record
@@ -104,12 +105,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
     // With split, attn_rows.cu's kernel is the one before. It waited before it let this one start, so
     // what this one reads is there, and the two may run side by side; the first CTA waits for it at
     // its end, and lets the next kernel start no sooner.
-    if (!p.split) {
+    if constexpr (!SPLIT) {
         griddep_wait();
         griddep_launch();
     }
     auto leave = [&] {
-        if (p.split && blockIdx.x == 0) {
+        if (SPLIT && blockIdx.x == 0) {
             griddep_wait();
             griddep_launch();
         }
@@ -122,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
     // units: 126.6 and 132.7).
     Seq own = tid < p.B ? seq_of(p, tid, blockIdx.x == 0) : Seq{0, 0, 0};
     int64_t all_work = 0;
-    if (p.split) {
+    if constexpr (SPLIT) {
         all_work = rows_work(own, p);
         for (int b = tid + kThreads; b < p.B; b += kThreads) all_work += rows_work(seq_of(p, b, false), p);
         all_work = warp_sum(all_work);
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>()) k_attn(const Attn
     }
     // a sequence; without query tokens if the other kernel has it
     auto left = [&](Seq s) {
-        if (p.split && takes_rows(s, p, all_work)) s.nq = 0;
+        if (SPLIT && takes_rows(s, p, all_work)) s.nq = 0;
         return s;
     };
     own = left(own);
@@ -781,15 +782,22 @@ size_t smem_bytes(int grid) {
     return (size_t)kWarps * kStages * 2 * 18 * D + (rows > factors ? rows : factors);
 }
 
-template <int D, int NT, bool F16>
-cudaError_t attn_of(const AttnParams& p, int grid, cudaStream_t s) {
+template <int D, int NT, bool F16, bool SPLIT>
+cudaError_t attn_kernel(const AttnParams& p, int grid, cudaStream_t s) {
     static std::atomic<bool> done[64];
     const size_t smem = smem_bytes<D, NT>(grid);
     const cudaError_t e = once_per_device(done, [smem] {
-        return cudaFuncSetAttribute(k_attn<D, NT, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        return cudaFuncSetAttribute(k_attn<D, NT, F16, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     });
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_attn<D, NT, F16>, dim3(grid), dim3(kThreads), smem, s, 1, p);
+    return launch_pdl(k_attn<D, NT, F16, SPLIT>, dim3(grid), dim3(kThreads), smem, s, 1, p);
+}
+
+template <int D, int NT, bool F16>
+cudaError_t attn_of(const AttnParams& p, int grid, cudaStream_t s) {
+    if constexpr (D == 128)
+        if (p.split) return attn_kernel<D, NT, F16, true>(p, grid, s);
+    return attn_kernel<D, NT, F16, false>(p, grid, s);
 }
 
 // Eights of query rows that a CTA holds. More rows share a step's conversions, up to what the

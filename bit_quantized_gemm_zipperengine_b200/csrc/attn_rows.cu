@@ -98,7 +98,8 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
 // Byte of 16-byte piece c of row n in a [rows][64 elements] block with 128-byte swizzle.
 __device__ __forceinline__ int swizzled(int n, int c) { return n * 128 + ((c ^ (n & 7)) << 4); }
 
-template <bool F16>
+// SPLIT: attn.cu's kernel has some of the sequences.
+template <bool F16, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_rows(const AttnParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint64_t q_full[kGroups], k_full[2], v_full[2];
@@ -143,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_rows(const AttnParams p) {
     if (warp == 0) {
         const Seq own = lane < p.B ? seq_of(p, lane, blockIdx.x == 0) : Seq{0, 0, 0};
         int64_t all_work = 0;
-        if (p.split) {
+        if constexpr (SPLIT) {
             all_work = rows_work(own, p);
             for (int b = lane + 32; b < p.B; b += 32) all_work += rows_work(seq_of(p, b, false), p);
             all_work = warp_sum(all_work);
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_rows(const AttnParams p) {
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             const int b = b0 + lane;
             Seq s = b0 == 0 ? own : b < p.B ? seq_of(p, b, blockIdx.x == 0) : Seq{0, 0, 0};
-            if (p.split && !takes_rows(s, p, all_work)) s.nq = 0;
+            if (SPLIT && !takes_rows(s, p, all_work)) s.nq = 0;
             const int64_t n = (int64_t)((s.nq * G.d + kBlock - 1) / kBlock) * H;
             int64_t x = n;
 #pragma unroll
@@ -473,13 +474,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_rows(const AttnParams p) {
     if (warp == 0) tmem_dealloc(tmem, kGroups * kCols);
 }
 
-template <bool F16>
+template <bool F16, bool SPLIT>
 cudaError_t rows_of(const AttnParams& p, unsigned grid, cudaStream_t s) {
     static std::atomic<bool> done[64];
     const cudaError_t e = once_per_device(
-        done, [] { return cudaFuncSetAttribute(k_attn_rows<F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
+        done, [] { return cudaFuncSetAttribute(k_attn_rows<F16, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_attn_rows<F16>, dim3(grid), dim3(kThreads), kSmem, s, 1, p);
+    return launch_pdl(k_attn_rows<F16, SPLIT>, dim3(grid), dim3(kThreads), kSmem, s, 1, p);
 }
 
 }  // namespace
@@ -513,7 +514,8 @@ cudaError_t launch_attn_rows(const AttnParams& p, bool f16, cudaStream_t s) {
     // at most: every sequence that is taken ends in a part of a tile
     const int64_t taken = p.split ? std::min<int64_t>(p.B, rows / p.least) : p.B;
     const unsigned grid = (unsigned)((rows / kBlock + taken) * p.cache.heads);
-    return f16 ? rows_of<true>(p, grid, s) : rows_of<false>(p, grid, s);
+    if (p.split) return f16 ? rows_of<true, true>(p, grid, s) : rows_of<false, true>(p, grid, s);
+    return f16 ? rows_of<true, false>(p, grid, s) : rows_of<false, false>(p, grid, s);
 }
 
 }  // namespace mq
