@@ -108,6 +108,11 @@ double real(PyObject* o) {
     if (v == -1.0 && PyErr_Occurred()) throw std::bad_exception();
     return v;
 }
+bool truth(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw std::bad_exception();
+    return v != 0;
+}
 template <typename P>
 P* pointer(PyObject* o) {
     return o == Py_None ? nullptr : reinterpret_cast<P*>(integer(o));
@@ -176,7 +181,7 @@ PyObject* py_gemv(PyObject*, PyObject* const* a, Py_ssize_t n) {
             ws = at::empty({(int64_t)need}, X.options().dtype(at::kByte));
         }
         return done(lib.gemv(X.data_ptr(), c.code, X.stride(0), pointer<mq_nvfp4_mat>(a[5]), pointer<mq_residual_packed>(a[6]),
-                             Y.data_ptr(), Y.stride(0), extent(X.size(0)), (int)N, (int)K, (unsigned)integer(a[7]),
+                             Y.data_ptr(), Y.stride(0), extent(X.size(0)), (int)N, (int)K, (unsigned)integer32(a[7]),
                              ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? (size_t)ws.numel() : 0, d.stream),
                     "mq_gemv");
     });
@@ -206,7 +211,7 @@ PyObject* py_qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const void *wq = array<void>(a[6], "q_weight", c.type, D, c.dev), *wk = array<void>(a[7], "k_weight", c.type, D, c.dev);
         OnDevice d(c.dev, a[10]);
         return done(lib.qk_norm_rope(q.p, k.p, qo.p, ko.p, extent(T), extent(D), c.code, wq, wk, (float)real(a[8]), t.pos, t.freq,
-                                     t.rot, PyObject_IsTrue(a[9]), d.stream),
+                                     t.rot, truth(a[9]), d.stream),
                     "mq_qk_norm_rope");
     });
 }
@@ -244,7 +249,7 @@ PyObject* py_qkv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t* slots = array<int64_t>(a[11], "slots", at::kLong, T, c.dev);
         OnDevice d(c.dev, a[14]);
         return done(lib.qkv_append(q.p, k.p, v.p, qo.p, ko.p, extent(T), c.code, wq, wk, (float)real(a[9]), t.pos, t.freq, t.rot,
-                                   PyObject_IsTrue(a[10]), slots, kv, d.stream),
+                                   truth(a[10]), slots, kv, d.stream),
                     "mq_qkv_append");
     });
 }

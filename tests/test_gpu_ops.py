@@ -283,6 +283,26 @@ def test_norm_rope_output_layouts(T, Hq, dev, mosaic):
         assert torch.equal(o, want), (st, sh)
 
 
+def test_binding_arguments_that_are_no_numbers(dev, mosaic):
+    """A flag or truth value that cannot be taken is an error of the call, and nothing is launched."""
+    q = torch.ones(2, 2, 64, dtype=BF, device=dev)
+    out = torch.zeros_like(q)
+    base, packed = ref.random_weight(64, 64, 0, 1, dev)
+    x, y = torch.ones(1, 64, dtype=BF, device=dev), torch.zeros(1, 64, dtype=BF, device=dev)
+    at = mosaic.mq_launch_count()
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        mosaic.mq_qk_norm_rope(q, None, out, None, interleaved=torch.zeros(2))
+    with pytest.raises(TypeError):
+        mosaic.mq_qk_norm_rope(q, None, out, None, eps="small")
+    for flags in (2 ** 32, 2 ** 33 + 4, -2 ** 40):
+        with pytest.raises(mosaic.MosaicError):
+            mosaic.mq_gemv(x, mosaic.Weight(base, packed), y, flags)
+    with pytest.raises(TypeError):
+        mosaic.mq_gemv(x, mosaic.Weight(base, packed), y, "base")
+    torch.cuda.synchronize()
+    assert mosaic.mq_launch_count() == at and (out == 0).all() and (y == 0).all()
+
+
 def test_rope_far_positions_and_zero_rows(dev, mosaic):
     q, k, _, w, pos, freq = rope_inputs(8, 2, 1, 128, HF, 3, dev)
     pos = torch.tensor([0, 1, -5, 2 ** 20, 2 ** 31, 2 ** 40, -(2 ** 33), 7], device=dev)
