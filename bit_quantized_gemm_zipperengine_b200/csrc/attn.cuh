@@ -66,7 +66,7 @@ __device__ __forceinline__ float lse_of(float top, float sum) {
 // hold kRowsWorth each then) if its chain of steps is not longer than an SM's even share of what
 // all such sequences cost in the other kernel. Both kernels find the same answer, from integers.
 constexpr int kRowsTile = 256, kRowsStep = 64, kRowsWorth = 48;
-constexpr int kRowsLeast = 128;  // `least` where the numbers of query tokens differ; below it where they do not
+constexpr int kRowsLeast = 56;  // `least` where the numbers of query tokens differ; below it where they do not
 
 __device__ __forceinline__ int64_t rows_steps(const Seq& s, const AttnParams& p) {
     return (p.window > 0 ? min((int64_t)s.len, (int64_t)p.window + s.nq) : (int64_t)s.len) / kRowsStep + 1;

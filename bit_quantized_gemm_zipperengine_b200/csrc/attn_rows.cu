@@ -98,6 +98,65 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
 // Byte of 16-byte piece c of row n in a [rows][64 elements] block with 128-byte swizzle.
 __device__ __forceinline__ int swizzled(int n, int c) { return n * 128 + ((c ^ (n & 7)) << 4); }
 
+// The CTA's tile, into work (its sequence, -1 for none; its number there): sequences in order, then
+// tiles from the last rows on (they see most), then heads. One warp looks through up to 32
+// sequences, all of them (with two barriers a round) through more.
+template <bool SPLIT>
+__device__ __forceinline__ void find_tile(const AttnParams& p, int* work, int64_t* sums) {
+    constexpr int kWarps = kThreads / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const bool few = p.B <= 32, first = blockIdx.x == 0;  // the first CTA reports what is out of range
+    if (few && warp > 0) return;
+    const int stride = few ? 32 : kThreads;
+    const Seq own = tid < p.B ? seq_of(p, tid, first) : Seq{0, 0, 0};
+    int64_t all_work = 0;
+    if constexpr (SPLIT) {
+        all_work = rows_work(own, p);
+        for (int b = tid + stride; b < p.B; b += stride) all_work += rows_work(seq_of(p, b, false), p);
+        all_work = warp_sum(all_work);
+        if (!few) {
+            if (lane == 0) sums[warp] = all_work;
+            __syncthreads();
+            all_work = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) all_work += sums[w];
+            __syncthreads();
+        }
+    }
+    int64_t base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += stride) {
+        const int b = b0 + tid;
+        Seq s = b0 == 0 ? own : b < p.B ? seq_of(p, b, first) : Seq{0, 0, 0};
+        if (SPLIT && !takes_rows(s, p, all_work)) s.nq = 0;
+        const int64_t n = (int64_t)((s.nq * p.by_group.d + kBlock - 1) / kBlock) * p.cache.heads;
+        int64_t x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        int64_t all = __shfl_sync(0xffffffffu, x, 31);
+        x += base;
+        if (!few) {
+            if (lane == 31) sums[warp] = all;
+            __syncthreads();
+            all = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                x += w < warp ? sums[w] : 0;
+                all += sums[w];
+            }
+            __syncthreads();
+        }
+        if (n > 0 && (int64_t)blockIdx.x >= x - n && (int64_t)blockIdx.x < x) {
+            work[0] = b;
+            work[1] = (int)(blockIdx.x - (x - n));
+        }
+        base += all;
+        if (!first && (int64_t)blockIdx.x < base) break;
+    }
+}
+
 // SPLIT: attn.cu's kernel has some of the sequences.
 template <bool F16, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_rows(const AttnParams p) {
@@ -106,10 +165,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_rows(const AttnParams p) {
     __shared__ uint64_t s_full[kGroups][2], s_free[kGroups], p_full[kGroups][2], done[kGroups][2];
     __shared__ uint32_t tmem_at;
     __shared__ int work[2];
+    __shared__ int64_t sums[kThreads / 32];
     __shared__ volatile int lost[4][4];  // of step i at i % 4: written before its keys, read before step i + 4's keys
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int H = p.cache.heads;
     const FastDiv& G = p.by_group;
+    if (tid == 0) work[0] = -1;
+    if constexpr (SPLIT) {
+        // a CTA without a tile leaves at once: the grid has one for every part that sequences may end in
+        __syncthreads();
+        griddep_wait();
+        find_tile<SPLIT>(p, work, sums);
+        __syncthreads();
+        if (work[0] < 0) {
+            griddep_launch();
+            return;
+        }
+    }
     // Tensor memory before the next kernel may start: it could take what is left of it.
     if (warp == 0) {
         tmem_alloc(&tmem_at, kGroups * kCols);
@@ -129,7 +201,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_rows(const AttnParams p) {
                 mbar_init(&done[g][b], 1);
             }
         }
-        work[0] = -1;
     }
     mbar_fence_init();
     tc_fence_before();
@@ -137,40 +208,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_rows(const AttnParams p) {
     tc_fence_after();
     const uint32_t tmem = tmem_at;
     const bool placed = (smem_u32(smem) & 1023u) == 0;  // the swizzle repeats every 1024 bytes
-    griddep_wait();
+    if constexpr (!SPLIT) griddep_wait();
     griddep_launch();
 
-    // The CTA's tile: sequences in order, then tiles from the last rows on (they see most), then heads.
-    if (warp == 0) {
-        const Seq own = lane < p.B ? seq_of(p, lane, blockIdx.x == 0) : Seq{0, 0, 0};
-        int64_t all_work = 0;
-        if constexpr (SPLIT) {
-            all_work = rows_work(own, p);
-            for (int b = lane + 32; b < p.B; b += 32) all_work += rows_work(seq_of(p, b, false), p);
-            all_work = warp_sum(all_work);
-        }
-        int64_t base = 0;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            const int b = b0 + lane;
-            Seq s = b0 == 0 ? own : b < p.B ? seq_of(p, b, blockIdx.x == 0) : Seq{0, 0, 0};
-            if (SPLIT && !takes_rows(s, p, all_work)) s.nq = 0;
-            const int64_t n = (int64_t)((s.nq * G.d + kBlock - 1) / kBlock) * H;
-            int64_t x = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += y;
-            }
-            x += base;
-            if (n > 0 && (int64_t)blockIdx.x >= x - n && (int64_t)blockIdx.x < x) {
-                work[0] = b;
-                work[1] = (int)(blockIdx.x - (x - n));
-            }
-            base = __shfl_sync(0xffffffffu, x, 31);
-            if (blockIdx.x != 0 && (int64_t)blockIdx.x < base) break;  // CTA 0 checks every sequence
-        }
-        if (!placed && lane == 0) report_index(p.err);
-    }
+    if constexpr (!SPLIT) find_tile<SPLIT>(p, work, sums);
+    if (!placed && tid == 0) report_index(p.err);
     __syncthreads();
     if (work[0] >= 0 && placed) {
         const Seq s = seq_of(p, work[0], false);
@@ -492,11 +534,12 @@ cudaError_t rows_of(const AttnParams& p, unsigned grid, cudaStream_t s) {
 // and 128 tokens behind 8192: 160 and 173, 161 and 102). A sequence that fills the SMs by itself is
 // never worse off here, however long it is. If none does, or the numbers of query tokens differ,
 // the kernels share the call, sequence by sequence (us by the average of all sequences and by each
-// one's own rows: a prompt of 2048 beside 15 single tokens behind 131072, 64/8 heads: 1930 and 546;
+// one's own rows: a prompt of 2048 beside 15 single tokens behind 131072, 64/8 heads: 1930 and 545;
 // beside one behind 2^20, 32/8 heads: 14500 and 296; 512 tokens beside 15 single ones, all behind
-// 8192: 239 and 163; 16 x 8 tokens behind 4096, one of them behind 131072, 64/8 heads: 1820 and
-// 251). A call that is all one kernel's pays 1 to 2% for it (16 x 8 behind 4096: 66.8 and 67.0; 32 x
-// 16 behind 2048: 72.2 and 73.6; eight prompts of 37 to 4000 tokens: 295 and 301).
+// 8192: 239 and 164; 16 x 8 tokens behind 4096, one of them behind 131072, 64/8 heads: 1820 and
+// 250; 1000 sequences of 1 to 20 tokens behind 500: 1393 and 1038). A call that is all one kernel's
+// pays up to 2 us, or 2%, for it (prompts of 1000 and 1024 tokens: 42 and 44; eight of 37 to 4000:
+// 294 and 300; 32 x 16 behind 2048: 71.8 and 73.4).
 AttnPlan attn_plan(const AttnParams& p, int D, int max_q) {
     const int64_t G = p.q.heads / p.cache.heads, H = p.cache.heads, rows = p.T * G;  // rows: of a cache head
     const int64_t fill = (int64_t)kRowsWorth * device_sms();
