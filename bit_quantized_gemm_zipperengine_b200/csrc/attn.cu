@@ -7,7 +7,8 @@
 //
 // Once a long cache streams, the conversions, multiplies and products that share the issue slots
 // are the longer half: 4 x 131072 tokens, 64/8 heads take 127 us (4.8 TB/s), the copies alone
-// 104, the arithmetic alone 122. One sequence of 509 tokens takes 9.8 us, all latency.
+// 104, the arithmetic alone 122; half of the issue slots are used, the rest are waits. One sequence
+// of 509 tokens takes 9.8 us, all latency.
 //
 // One pass. A warp takes 32 tokens at a time: two records of the cache, one bulk copy each,
 // into its own ring in shared memory. Its products run on the tensor cores with the

@@ -2,9 +2,9 @@
 //   Y[m,n] = rn(g_w * sum_k x[m,k] (wh[n,k] + [block selected] rh[n,k])),  wh = val * dec(sf).
 //
 // What bounds it: the weight's bytes (9/16 a weight, 2304 a residual block), read once, and
-// with them the conversions and products, which fill half of the issue slots: 1 token through
-// 28672 x 8192 with a tenth of the blocks takes 37.7 us (3.9 TB/s), 16 through 5120 x 25600
-// 30.0 us (14.3 for the copies alone), 1 through 4096 x 4096 8.4 us (4.4).
+// waits: 1 token through 28672 x 8192 with a tenth of the blocks takes 37.7 us (3.9 TB/s; half of
+// the issue slots and no pipe more than 43% used), 16 through 5120 x 25600 30.0 us (14.3 for the
+// copies alone), 1 through 4096 x 4096 8.4 us (4.4).
 //
 // The work of 64 weight rows is a list of steps: 256 columns of the base each, then four
 // residual blocks each (a block row's blocks lie one behind the other). In both a lane of

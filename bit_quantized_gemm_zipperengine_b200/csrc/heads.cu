@@ -10,7 +10,7 @@
 // bytes each: the sum of squares is a shuffle tree, the partner of a rotated half sits
 // rot/16 lanes away, and a group of 16 quantized elements is a lane pair. A warp's next row is
 // in flight while it works on one. 16 tokens of 72 heads take 2.3 us; 8191 of 40 heads, turned,
-// 30.8 us (5.5 TB/s; 71% of the issue slots used), and appended, 8 heads, about 15 us (74%, ~40
+// 30.8 us (5.5 TB/s; 71% of the issue slots used), and appended, 8 heads, about 15 us (76%, ~40
 // instructions for eight quantized values).
 #include <algorithm>
 

@@ -106,7 +106,9 @@ mq_status mq_qk_norm_rope(const mq_heads* q, const mq_heads* k, const mq_heads* 
 /*
  * Quantizes K and V rows [T][cache heads][D] into the cache at slots[t]. A negative slot
  * skips its token (padding); one past the cache is skipped and reported. The slots of one
- * call are distinct: a slot named twice ends up with a mixture of its rows.
+ * call are distinct: a slot named twice ends up with a mixture of its rows. The rows are finite,
+ * as mosaic.h's inputs are: sixteen NaN in a row of v would also reach query rows that do not see
+ * their token, where others of their sequence do.
  */
 mq_status mq_kv_append(const mq_heads* k, const mq_heads* v, int T, mq_dtype type, const int64_t* slots,
                        const mq_kv_cache* cache, mq_stream stream);
@@ -147,7 +149,7 @@ size_t mq_kv_attention_workspace_bytes(int q_heads, int kv_heads, int D, int max
  *   out = sum_j softmax_j(scale * q . K_j) V_j,   lse = ln sum_j exp(scale * q . K_j).
  * Query head h reads cache head h / (q heads / cache heads). A row that sees nothing gets
  * zeros (lse -inf). Scores, softmax sums and outputs are held in fp32; the softmax weights
- * enter the second product in fp16. Rows of q that belong to no sequence leave out and lse
+ * enter the second product in fp16, and bf16 queries the first one as mq_gemv's activations do. Rows of q that belong to no sequence leave out and lse
  * as they were. A page outside the cache, a length past the table (or 2^30) or a row past T is
  * left out and reported. q, out: [T][q heads][D] (distinct); lse: fp32 [T][q heads] or NULL.
  * max_q: the largest number of query tokens of a sequence that the caller expects (it sizes
