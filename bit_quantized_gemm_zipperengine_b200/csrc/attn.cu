@@ -801,22 +801,24 @@ cudaError_t attn_of(const AttnParams& p, int grid, cudaStream_t s) {
     return attn_kernel<D, NT, F16, false>(p, grid, s);
 }
 
-// Eights of query rows that a CTA holds. More rows share a step's conversions, up to what the
-// registers hold; with few rows the shorter step wins (8 sequences of up to 4001 tokens and 24
-// rows: 26.4 us by 16, 29.0 by 24; 512 rows: 157 and 143 us).
-int row_tiles(int q_heads, int kv_heads, int max_q) {
-    const int64_t rows = (int64_t)(q_heads / kv_heads) * max_q;
-    return rows <= 8 ? 1 : rows <= 32 ? 2 : 3;
-}
-
 int grid_of(int nt) { return device_sms() * (nt == 1 ? ctas_per_sm<1>() : ctas_per_sm<2>()); }
+
+// Eights of query rows that a CTA holds. More rows share a step's copies and conversions, up to what
+// the registers hold; with few steps a CTA the shorter step wins. So 17 to 24 rows are one tile where
+// the tables' capacity gives a CTA kLong units or more, and two of 16 below (us by 16 and by 24, 20
+// rows of 8 cache heads: 8 sequences of up to 4001 tokens, ragged, 26.4 and 29.0; of 4001 tokens 36.3
+// and 33.2; of 16384 97 and 81; of 65536 328 and 233); 25 to 32 rows are two of 16 (8 x 65536: 330
+// and 435), more rows tiles of 24 (8 sequences of 512 rows: 157 and 143).
+constexpr int kLong = 8;
+int row_tiles(int64_t rows, bool many_units) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 && many_units ? 3 : rows <= 32 ? 2 : 3; }
 
 }  // namespace
 
 // Counters first, in the same place for every shape: the partial sums of one must not fall on
 // the counters of another that shares the workspace.
 size_t attn_workspace(int q_heads, int kv_heads, int D, int max_q, size_t* partials_at) {
-    const int nt = row_tiles(q_heads, kv_heads, max_q);
+    const int64_t rows = (int64_t)(q_heads / kv_heads) * max_q;
+    const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 3;  // what fewer rows need, fits too
     *partials_at = ((size_t)device_sms() * ctas_per_sm<1>() * sizeof(int) + 255) / 256 * 256;
     return *partials_at + (size_t)2 * grid_of(nt) * slot_floats(nt, D) * sizeof(float);
 }
@@ -827,7 +829,10 @@ cudaError_t launch_attn(const AttnParams& p0, int D, int max_q, bool f16, cudaSt
     p.by_page = FastDiv(p.cache.page_size);
     p.scale *= 1.4426950408889634f;  // scores in powers of two
     const AttnPlan plan = attn_plan(p, D, max_q);
-    int nt = row_tiles(p.q.heads, p.cache.heads, max_q);
+    const int64_t G = p.q.heads / p.cache.heads;
+    const int64_t units = (int64_t)p.max_pages * p.cache.page_size / kUnit * p.B * p.cache.heads;
+    const bool many_units = units >= (int64_t)kLong * grid_of(2);
+    int nt = row_tiles(G * max_q, many_units);
     if (plan.rows) {
         p.split = plan.other;
         p.least = plan.least;
@@ -835,7 +840,7 @@ cudaError_t launch_attn(const AttnParams& p0, int D, int max_q, bool f16, cudaSt
         const cudaError_t e = launch_attn_rows(p, f16, s);
         if (e != cudaSuccess || !p.split) return e;
         *kernels = 2;
-        if (plan.least == kRowsLeast) nt = std::min(nt, row_tiles(p.q.heads, p.cache.heads, 1));  // mostly single tokens are left
+        if (plan.least == kRowsLeast) nt = std::min(nt, row_tiles(G, many_units));  // mostly single tokens are left
     }
     const int grid = grid_of(nt);
     p.by_grid = FastDiv(grid);

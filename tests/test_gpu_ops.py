@@ -831,6 +831,27 @@ def test_attention_missing_pages_are_left_out(lens, Hq, H, D, P, bad, dev, mosai
         within(lse, want[1], bl, "lse")
 
 
+@pytest.mark.parametrize("lens,nqs,Hq,H,D,window", [
+    ([515, 64], [1, 1], 20, 1, 128, 0), ([3001, 40, 7], [5, 5, 5], 16, 4, 128, 0), ([900, 2, 300], [3, 3, 3], 16, 2, 64, 70),
+    ([700, 61], [4, 6], 32, 8, 64, 0), ([1500, 30], [17, 1], 2, 2, 128, 0)])
+def test_attention_tables_of_great_capacity(lens, nqs, Hq, H, D, window, dev, mosaic):
+    """17 to 24 query rows, with tables as long as the sequences and with far longer ones: another
+    tile of rows, the same attention; one workspace serves both."""
+    q, pages, ks, vs, table, kv_len, cu = attn_inputs(lens, nqs, Hq, H, D, 16, BF, 240 + D + Hq, dev)
+    want = ref.attention(q, pages, ks, vs, table, lens, nqs, 0.09, window)
+    bo, bl = attn_bounds(*want, BF, lens)
+    dead = want[1] == -math.inf
+    sms = torch.cuda.get_device_properties(dev).multi_processor_count
+    wide = torch.full((len(lens), -(-8 * 2 * sms * 128 // (16 * H * len(lens))) + 8), -1, dtype=torch.int32, device=dev)
+    wide[:, :table.shape[1]] = table
+    ws = mosaic.kv_attention_workspace(q, mosaic.KVCache(pages, ks, vs), max(nqs))
+    for t in (table, wide, table):
+        o, lse = run_attn(mosaic, q, pages, ks, vs, t, kv_len, cu, max(nqs), 0.09, window, BF, ws=ws)
+        within(o, want[0], bo, "out")
+        assert (lse[dead] == -math.inf).all() and (o[dead] == 0).all()
+        within(lse[~dead], want[1][~dead], bl[~dead], "lse")
+
+
 def test_attention_shapes_share_a_workspace(dev, mosaic):
     """Calls of different shapes take turns on one workspace, large enough for each: the partial
     sums of one leave the other's counters alone."""
