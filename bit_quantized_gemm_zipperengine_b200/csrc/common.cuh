@@ -33,6 +33,12 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// What an earlier kernel may have written while this one was already launched: an ordinary load,
+// which stays behind griddep_wait and sees what that waited for. __ldg promises that memory does
+// not change while the kernel lives, which such memory does, and may be moved up before the wait.
+template <typename T>
+__device__ __forceinline__ T ld_prior(const T* p) { return *p; }
+
 // ---------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_ctarank() {
     uint32_t r;

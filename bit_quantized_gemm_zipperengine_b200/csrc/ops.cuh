@@ -60,12 +60,6 @@ __device__ __forceinline__ int rec_vscale(int i, int q) {
     return 17 * D + q * 16 + ((i & 7) >> 1) * 4 + ((i >> 3) << 1) + (i & 1);
 }
 
-// What an earlier kernel may have written while this one was already launched: an ordinary load,
-// which stays behind griddep_wait and sees what that waited for. __ldg promises that memory does
-// not change while the kernel lives, which such memory does, and may be moved up before the wait.
-template <typename T>
-__device__ __forceinline__ T ld_prior(const T* p) { return *p; }
-
 // Records an index that a kernel found out of range in the device error word.
 __device__ __forceinline__ void report_index(int* err) { atomicCAS(err, 0, (int)MQ_ERR_INVALID_ARG); }
 

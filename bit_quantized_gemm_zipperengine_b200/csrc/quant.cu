@@ -34,7 +34,7 @@ __device__ __forceinline__ uint4 ld_stream16_hint(const uint4* p, uint64_t polic
 // estimate, which it does not use). It waits for that kernel only at its end, so that
 // its own completion still implies the predecessor's. The partials it overwrites are
 // read by the quantizers before they let their dependents start.
-__global__ void __launch_bounds__(512, 1) k_amax_partial(const uint16_t* __restrict__ W, int64_t n8,
+__global__ void __launch_bounds__(512, 1) k_amax_partial(const uint16_t* W, int64_t n8,
                                                       float* __restrict__ partial) {
     griddep_launch();
     float m = 0.0f;
@@ -84,8 +84,8 @@ __global__ void __launch_bounds__(512, 1) k_amax_partial(const uint16_t* __restr
 // One thread per group; the group count is a multiple of 32 (K % 64 == 0 and
 // N % 64 == 0), so whole warps stay together for the 4-group scale gather. The groups of
 // the rows past N up to the next multiple of 128 write zero tiled scales.
-__global__ void __launch_bounds__(256) k_quant_weight(const uint16_t* __restrict__ W, int N, int K,
-                                                      const float* __restrict__ partial,
+__global__ void __launch_bounds__(256) k_quant_weight(const uint16_t* W, int N, int K,
+                                                      const float* partial,
                                                       uint8_t* __restrict__ codes, uint8_t* __restrict__ sf,
                                                       uint8_t* __restrict__ sf_swz, float* __restrict__ g_out,
                                                       uint8_t* __restrict__ rcodes, uint8_t* __restrict__ rsf) {
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(256) k_quant_weight(const uint16_t* __restrict
 // whose X and outputs are not touched by the kernels still running before it.
 template <int kGPT>
 __global__ void __launch_bounds__(1024)
-    k_quant_act(const uint16_t* __restrict__ X, int M, int K, uint8_t* __restrict__ codes,
+    k_quant_act(const uint16_t* X, int M, int K, uint8_t* __restrict__ codes,
                 uint8_t* __restrict__ sf, uint8_t* __restrict__ sf_swz, float* __restrict__ g_x, int early) {
     if (!early) griddep_wait();
     griddep_launch();
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(1024)
 //   h = 4, 2, 1    warps, in shared memory, one thread per column.
 constexpr int kHMaxTokens = 1024;
 template <int NB>
-__global__ void __launch_bounds__(256) k_hessian(const uint16_t* __restrict__ X, int T, int K,
+__global__ void __launch_bounds__(256) k_hessian(const uint16_t* X, int T, int K,
                                                  float* __restrict__ H) {
     griddep_wait();
     griddep_launch();

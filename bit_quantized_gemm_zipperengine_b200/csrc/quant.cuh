@@ -16,7 +16,7 @@ constexpr int kAmaxBlocks = 148;
 // 16 bf16 values (32 bytes, 16-byte aligned) widened to fp32.
 __device__ __forceinline__ void load16_bf16(const uint16_t* p, float (&a)[16]) {
     const uint4* q = reinterpret_cast<const uint4*>(p);
-    const uint4 v0 = __ldg(q), v1 = __ldg(q + 1);
+    const uint4 v0 = ld_prior(q), v1 = ld_prior(q + 1);
     const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -31,7 +31,7 @@ __device__ __forceinline__ float tensor_scale(const float* partial) {
     __shared__ float s_g;
     if (threadIdx.x < 32) {
         float m = 0.0f;
-        for (int i = threadIdx.x; i < kAmaxBlocks; i += 32) m = fmaxf(m, __ldg(partial + i));
+        for (int i = threadIdx.x; i < kAmaxBlocks; i += 32) m = fmaxf(m, ld_prior(partial + i));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (threadIdx.x == 0) s_g = (m == 0.0f) ? 1.0f : __fdiv_rn(m, 2688.0f);
@@ -59,7 +59,7 @@ __device__ __forceinline__ uint32_t gather4(uint32_t b) {
 // group held in registers (kGPT groups per thread, groups tid + j * blockDim), so the row
 // is read once. Rows >= M only clear their tiled scales.
 template <int kGPT>
-__device__ __forceinline__ void quant_act_row(const uint16_t* __restrict__ X, int M, int K,
+__device__ __forceinline__ void quant_act_row(const uint16_t* X, int M, int K,
                                               uint8_t* __restrict__ codes, uint8_t* __restrict__ sf,
                                               uint8_t* __restrict__ sf_swz, float* __restrict__ g_x, int m) {
     const int G = K / 16;

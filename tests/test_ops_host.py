@@ -176,15 +176,15 @@ def test_attention_refusals(L, buf):
 
 
 def test_read_only_loads_are_of_final_data_alone():
-    """The operators' kernels start before their predecessor ends. __ldg promises that what it reads
+    """The operators' kernels, and the quantizer of prompts, start before their predecessor ends. __ldg promises that what it reads
     does not change while the kernel lives: only the packed weight, whose writers ended before."""
     csrc = os.path.join(build.PKG, "csrc")
-    for name in ("attn.cu", "attn.cuh", "attn_rows.cu", "gemv.cu", "heads.cu", "half_mma.cuh", "ops.cuh"):
+    for name in ("attn.cu", "attn.cuh", "attn_rows.cu", "gemv.cu", "heads.cu", "half_mma.cuh", "ops.cuh", "quant.cu", "quant.cuh"):
         with open(os.path.join(csrc, name)) as f:
             code = re.sub(r"//[^\n]*", "", f.read())
         read = set(re.findall(r"__ldg\(\s*([\w.]+)", code))
         assert read <= ({"p.tile_ptr", "p.blk_kt", "p.g_w"} if name == "gemv.cu" else set()), (name, read)
-        assert "__restrict__" not in code, name  # a const __restrict__ pointer makes the same promise
+        assert not re.search(r"const \w+\* __restrict__", code), name  # makes the same promise
 
 
 def test_attention_layer_keeps_one_workspace_a_stream(L, monkeypatch):
